@@ -26,11 +26,32 @@ Entry points (same names as the C ABI):
                                              intermediates live in a per-GPU scratch array
                                              (problems up to kda_noalloc_scratch_bytes())
   kda_last_error()                           reason for the last failure
-Every entry point takes ``debug=True`` (except the allocation-free one): wait for the call
+and, around the mixer:
+  kda_conv_fwd / kda_conv_bwd                short causal convolution with bias and SiLU
+                                             (prompts, packed batches, decode steps; gradients)
+  kda_ssm_chunk_fwd / kda_ssm_recurrent_fwd  selective state space scan: one decay per head, no
+                                             erase (prompts; token by token)
+  kda_rmsnorm_fwd / kda_rmsnorm_bwd          RMS norm with the residual's addition; gradients
+  kda_rmsnorm_quant_fwd                      the same norm with an e4m3 output and its scales
+Every entry point that takes offsets takes ``debug=True`` (except the allocation-free one): wait for the call
 and raise KdaDeviceCheckError when a device-side check flagged the inputs.
 """
 from __future__ import annotations
 
+from ._layer import (  # noqa: F401
+    KDA_ACT_NONE,
+    KDA_ACT_SILU,
+    kda_conv_bwd,
+    kda_conv_bwd_workspace_bytes,
+    kda_conv_fwd,
+    kda_rmsnorm_bwd,
+    kda_rmsnorm_bwd_workspace_bytes,
+    kda_rmsnorm_fwd,
+    kda_rmsnorm_quant_fwd,
+    kda_ssm_chunk_fwd,
+    kda_ssm_chunk_fwd_workspace_bytes,
+    kda_ssm_recurrent_fwd,
+)
 from ._lib import (  # noqa: F401
     KDA_BF16,
     KDA_DEV_BAD_CU_SEQLENS,
@@ -73,4 +94,7 @@ __all__ = [
     "kda_noalloc_scratch_bytes", "KDA_BF16", "KDA_F32", "KDA_DEV_BAD_CU_SEQLENS", "load_library",
     "library_path", "KDA_GATE_LOG2", "KDA_GATE_RAW_F32", "KDA_GATE_RAW_BF16", "KDA_PRE_L2NORM_Q",
     "KDA_PRE_L2NORM_K", "KDA_PRE_BETA_SIGMOID", "KDA_PRE_NEG_EIGVAL", "KDA_STATE_KV", "KDA_STATE_VK",
+    "kda_conv_fwd", "kda_conv_bwd", "kda_conv_bwd_workspace_bytes", "kda_ssm_chunk_fwd",
+    "kda_ssm_chunk_fwd_workspace_bytes", "kda_ssm_recurrent_fwd", "kda_rmsnorm_fwd", "kda_rmsnorm_quant_fwd",
+    "kda_rmsnorm_bwd", "kda_rmsnorm_bwd_workspace_bytes", "KDA_ACT_NONE", "KDA_ACT_SILU",
 ]

@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libkda.so")
 CEILING_LIB = os.path.join(PKG, "libkda_ceiling.so")
 CEILING_SOURCE = "ceiling.hip"
 SOURCES = ["kda_api.cpp", "kda_recurrent.hip", "kda_chunk.hip", "kda_chunk_bwd.hip",
-           "kda_noalloc.hip"]
+           "kda_noalloc.hip", "kda_conv.hip", "kda_rmsnorm.hip", "kda_ssm_recurrent.hip",
+           "kda_ssm_chunk.hip", "kda_layer_api.cpp"]
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 

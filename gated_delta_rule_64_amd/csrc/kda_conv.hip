@@ -1,0 +1,318 @@
+// Short causal depthwise convolution (W = 2..4 taps), with bias and SiLU, for gfx950:
+//     pre[t, d] = bias[d] + sum_i w[d, i] x[t - (W-1) + i, d],   y = pre sigmoid(pre) or pre,
+// rows before a sequence's first token coming from its state (the last W - 1 rows it saw),
+// and the gradients of it. The layer's q, k and v (or x, b and c) go through it side by
+// side as channels, ahead of the delta rule or the state space scan.
+//
+// Nothing is reused but the W - 1 neighbours, so both directions are bound by HBM: x in and
+// y out, or x and dy in and dx out. A lane owns 16 bytes of a row (8 bf16 or 4 fp32
+// channels; one channel where rows are not whole 16-byte pieces) and walks TT rows of one
+// sequence with the window of the last W - 1 rows in registers, so a row is read once, and
+// the W - 1 rows before the tile once more (from L2: the neighbouring tile's lanes read
+// them). A wave is 64 such lanes side by side, one contiguous run of a row per access.
+#include "kda_layer.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int TT_FWD = 16;
+constexpr int TT_BWD = 32;
+
+// lanes of a block along the channels (a power of two, at most 64); the block's other lanes
+// take other tiles
+inline int lanes_along(int D, int vec) {
+    const int n = (D + vec - 1) / vec;
+    int l = 1;
+    while (l < n && l < 64) l *= 2;
+    return l;
+}
+
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void load_taps(const ConvArgs& a, int d, float (&w)[W][VEC], float (&bias)[VEC]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i][e] = load_scalar(a.weight, a.w_dtype, (long long)(d + e) * W + i);
+        bias[e] = a.bias ? load_scalar(a.bias, a.w_dtype, d + e) : 0.f;
+    }
+}
+
+// row `pos` (negative: rows of the state, or zeros) of a sequence
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void load_row(const ConvArgs& a, const SeqTile& s, int pos, int d, float (&o)[VEC]) {
+    if (pos >= 0) {
+        load_vec<VEC>(static_cast<const T*>(a.x) + (s.row0 + pos) * a.x_stride + d, o);
+    } else if (a.initial_state) {
+        load_vec<VEC>(static_cast<const T*>(a.initial_state) + ((long long)s.n * (W - 1) + (W - 1 + pos)) * a.D + d, o);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = 0.f;
+    }
+}
+
+template <typename T, int VEC, int W>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvArgs a, int along, int dblocks, long long tiles,
+                                                       int tiles_dense) {
+    if (blockIdx.x == 0) flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
+    const int dv = (int)(blockIdx.x % dblocks) * along + (threadIdx.x & (along - 1));
+    const long long tile = (long long)(blockIdx.x / dblocks) * (256 / along) + threadIdx.x / along;
+    const int d = dv * VEC;
+    if (d >= a.D || tile >= tiles) return;
+    const SeqTile s = seq_tile(tile, a.cu_seqlens, a.N, a.T, TT_FWD, tiles_dense);
+    if (s.len < 0) return;
+
+    float w[W][VEC], bias[VEC], win[W][VEC];
+    load_taps<T, VEC, W>(a, d, w, bias);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) load_row<T, VEC, W>(a, s, s.pos - (W - 1) + i, d, win[i]);
+
+    // the sequence's first tile hands on the last W - 1 rows it saw: before anything is
+    // written, since final_state may be initial_state, which no other tile reads
+    if (s.pos == 0 && a.final_state) {
+        float last[W - 1][VEC];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) load_row<T, VEC, W>(a, s, s.len - (W - 1) + j, d, last[j]);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            store_vec<VEC>(static_cast<T*>(a.final_state) + ((long long)s.n * (W - 1) + j) * a.D + d, last[j]);
+    }
+    const int end = s.len - s.pos < TT_FWD ? s.len - s.pos : TT_FWD;
+    const T* xp = static_cast<const T*>(a.x) + (s.row0 + s.pos) * a.x_stride + d;
+    T* yp = static_cast<T*>(a.y) + (s.row0 + s.pos) * (long long)a.D + d;
+#pragma unroll 4
+    for (int t = 0; t < end; ++t) {
+        load_vec<VEC>(xp + t * a.x_stride, win[W - 1]);
+        float out[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float acc = bias[e];
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc = fmaf(w[i][e], win[i][e], acc);
+            out[e] = a.silu ? acc * sigmoid_fast(acc) : acc;
+        }
+        store_vec<VEC>(yp + (long long)t * a.D, out);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) win[i][e] = win[i + 1][e];
+    }
+}
+
+// The gradients. A lane walks its tile's rows and the W - 1 after them (whose dpre it forms
+// again), with windows of x and of dpre: dx[t] = sum_i w[i] dpre[t + W-1-i], and while
+// t is one of its own rows, dw[i] += dpre[t] x[t - (W-1) + i] and db += dpre[t] in fp32.
+// The sequence's first tile also has the state's rows (positions -(W-1) .. -1).
+// The block adds its tiles' sums in LDS and leaves one row of partial sums; sum_rows adds
+// those in order, so results do not depend on scheduling.
+template <typename T, int VEC, int W>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int along, int dblocks, long long tiles,
+                                                       int tiles_dense, long long P) {
+    const ConvArgs& a = b.f;
+    extern __shared__ float sums[];   // [256 / along][W + 1][along * VEC]
+    if (blockIdx.x == 0) flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
+    const int ln = threadIdx.x & (along - 1), grp = threadIdx.x / along, groups = 256 / along;
+    const int d = ((int)(blockIdx.x % dblocks) * along + ln) * VEC;
+    const long long p = blockIdx.x / dblocks;
+    const bool live = d < a.D;
+    float w[W][VEC], bias[VEC], dw[W][VEC], db[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        db[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) dw[i][e] = 0.f;
+    }
+    if (live) load_taps<T, VEC, W>(a, d, w, bias);
+    for (long long tile = p * groups + grp; live && tile < tiles; tile += P * groups) {
+        const SeqTile s = seq_tile(tile, a.cu_seqlens, a.N, a.T, TT_BWD, tiles_dense);
+        if (s.len < 0) continue;
+        const int end = s.len - s.pos < TT_BWD ? s.len : s.pos + TT_BWD;   // own rows: s.pos .. end-1
+        const int first = s.pos == 0 ? -(W - 1) : s.pos;                   // rows whose gradient is written
+        float win[W][VEC], dp[W][VEC];                                    // x and dpre, the last W rows
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) load_row<T, VEC, W>(a, s, s.pos - (W - 1) + i, d, win[i]);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) dp[i][e] = 0.f;
+        for (int t = s.pos; t < end + W - 1; ++t) {
+            // dpre of row t (zero past the sequence)
+            if (t < s.len) {
+                load_row<T, VEC, W>(a, s, t, d, win[W - 1]);
+                load_vec<VEC>(static_cast<const T*>(b.dy) + (s.row0 + t) * (long long)a.D + d, dp[W - 1]);
+                if (a.silu) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        float acc = bias[e];
+#pragma unroll
+                        for (int i = 0; i < W; ++i) acc = fmaf(w[i][e], win[i][e], acc);
+                        const float sg = sigmoid_fast(acc);
+                        dp[W - 1][e] *= sg * (1.f + acc * (1.f - sg));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) dp[W - 1][e] = 0.f;
+            }
+            if (t < end) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    db[e] += dp[W - 1][e];
+#pragma unroll
+                    for (int i = 0; i < W; ++i) dw[i][e] = fmaf(dp[W - 1][e], win[i][e], dw[i][e]);
+                }
+            }
+            // row t - (W-1) has every term: dpre[t - (W-1) .. t] against w[W-1 .. 0]
+            const int r = t - (W - 1);
+            if (r >= first) {
+                float g[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    g[e] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) g[e] = fmaf(w[W - 1 - i][e], dp[i][e], g[e]);
+                }
+                const int j = r - (s.len - (W - 1));   // the row of the final state it is handed on as
+                if (b.dfinal && j >= 0) {
+                    float f[VEC];
+                    load_vec<VEC>(static_cast<const T*>(b.dfinal) + ((long long)s.n * (W - 1) + j) * a.D + d, f);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) g[e] += f[e];
+                }
+                if (r >= 0)
+                    store_vec<VEC>(static_cast<T*>(b.dx) + (s.row0 + r) * (long long)a.D + d, g);
+                else if (b.dinitial)
+                    store_vec<VEC>(static_cast<T*>(b.dinitial) + ((long long)s.n * (W - 1) + W - 1 + r) * a.D + d, g);
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    win[i][e] = win[i + 1][e];
+                    dp[i][e] = dp[i + 1][e];
+                }
+        }
+    }
+    const int cols = along * VEC;
+    float* mine = sums + (size_t)grp * (W + 1) * cols + ln * VEC;
+#pragma unroll
+    for (int i = 0; i <= W; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) mine[i * cols + e] = i < W ? dw[i < W ? i : 0][e] : db[e];
+    __syncthreads();
+    for (int k = threadIdx.x; k < (W + 1) * cols; k += 256) {
+        float acc = 0.f;
+        for (int g = 0; g < groups; ++g) acc += sums[(size_t)g * (W + 1) * cols + k];
+        const int i = k / cols, dd = (int)(blockIdx.x % dblocks) * cols + k % cols;
+        if (dd < a.D) b.partial[(p * (W + 1) + i) * a.D + dd] = acc;
+    }
+}
+
+// Sums of P rows of M partial sums: 64 columns x 4 quarters of the rows per block.
+__global__ __launch_bounds__(256) void sum_rows_kernel(const SumRows s) {
+    __shared__ float part[4][64];
+    const int ln = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const long long m = (long long)blockIdx.x * 64 + ln;
+    float acc = 0.f;
+    if (m < s.M) {
+        const long long each = (s.P + 3) / 4;
+        const long long p0 = q * each, p1 = p0 + each < s.P ? p0 + each : s.P;
+#pragma unroll 8
+        for (long long p = p0; p < p1; ++p) acc += s.part[p * s.M + m];
+    }
+    part[q][ln] = acc;
+    __syncthreads();
+    if (q != 0 || m >= s.M) return;
+    acc = (part[0][ln] + part[1][ln]) + (part[2][ln] + part[3][ln]);
+    const long long row = m / s.D;
+    const int d = (int)(m % s.D);
+    if (row < s.taps) s.out[(long long)d * s.taps + row] = acc;
+    else if (s.out_tail) s.out_tail[d] = acc;
+}
+
+inline long long tiles_of(int B, int T, int N, bool packed, int TT) {
+    if (N == 0) return 0;
+    return packed ? (long long)T / TT + N : (long long)B * ((T + TT - 1) / TT > 0 ? (T + TT - 1) / TT : 1);
+}
+inline int tiles_dense_of(int T, int TT) { return (T + TT - 1) / TT > 0 ? (T + TT - 1) / TT : 1; }
+
+// blocks along the rows of the backward: enough blocks to fill the chip, few partial sums
+inline long long bwd_rows_of_blocks(long long tiles, int groups, int dblocks) {
+    const long long most = (tiles + groups - 1) / groups;
+    long long want = (1024 + dblocks - 1) / dblocks;
+    return most < want ? (most > 0 ? most : 1) : want;
+}
+
+template <typename T, int VEC>
+hipError_t fwd_v(const ConvArgs& a) {
+    const int along = lanes_along(a.D, VEC);
+    const int dblocks = (a.D + along * VEC - 1) / (along * VEC);
+    const long long tiles = tiles_of(a.B, a.T, a.N, a.cu_seqlens != nullptr, TT_FWD);
+    const int groups = 256 / along;
+    const long long blocks = (tiles + groups - 1) / groups * dblocks;
+    if (blocks == 0) return hipSuccess;
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    const int td = tiles_dense_of(a.T, TT_FWD);
+    const dim3 grid((unsigned)blocks), block(256);
+    if (a.W == 4) hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, 4>), grid, block, 0, a.stream, a, along, dblocks, tiles, td);
+    else if (a.W == 3) hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, 3>), grid, block, 0, a.stream, a, along, dblocks, tiles, td);
+    else hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, 2>), grid, block, 0, a.stream, a, along, dblocks, tiles, td);
+    return hipGetLastError();
+}
+
+template <typename T, int VEC>
+hipError_t bwd_v(const ConvBwdArgs& b) {
+    const ConvArgs& a = b.f;
+    const int along = lanes_along(a.D, VEC);
+    const int dblocks = (a.D + along * VEC - 1) / (along * VEC);
+    const long long tiles = tiles_of(a.B, a.T, a.N, a.cu_seqlens != nullptr, TT_BWD);
+    const int groups = 256 / along;
+    const long long P = bwd_rows_of_blocks(tiles, groups, dblocks);
+    const long long blocks = P * dblocks;
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    const int td = tiles_dense_of(a.T, TT_BWD);
+    const dim3 grid((unsigned)blocks), block(256);
+    const size_t lds = (size_t)256 * VEC * (a.W + 1) * sizeof(float);
+    if (a.W == 4) hipLaunchKernelGGL((conv_bwd_kernel<T, VEC, 4>), grid, block, lds, a.stream, b, along, dblocks, tiles, td, P);
+    else if (a.W == 3) hipLaunchKernelGGL((conv_bwd_kernel<T, VEC, 3>), grid, block, lds, a.stream, b, along, dblocks, tiles, td, P);
+    else hipLaunchKernelGGL((conv_bwd_kernel<T, VEC, 2>), grid, block, lds, a.stream, b, along, dblocks, tiles, td, P);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    SumRows s;
+    s.part = b.partial; s.P = P; s.M = (long long)(a.W + 1) * a.D;
+    s.out = b.dweight; s.out_tail = b.dbias; s.D = a.D; s.taps = a.W;
+    return launch_sum_rows(s, a.stream);
+}
+
+}  // namespace
+
+hipError_t launch_sum_rows(const SumRows& s, hipStream_t stream) {
+    hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((s.M + 63) / 64)), dim3(256), 0, stream, s);
+    return hipGetLastError();
+}
+
+long long conv_bwd_partials(int B, int T, int D, int N, bool packed, int dtype) {
+    // the scalar and the 16-byte form differ in their blocks: room for either
+    long long most = 0;
+    for (int vec : {1, dtype == KDA_BF16 ? 8 : 4}) {
+        const int along = lanes_along(D, vec);
+        const int dblocks = (D + along * vec - 1) / (along * vec);
+        const long long P = bwd_rows_of_blocks(tiles_of(B, T, N, packed, TT_BWD), 256 / along, dblocks);
+        most = P > most ? P : most;
+    }
+    return most;
+}
+
+hipError_t launch_conv_fwd(const ConvArgs& a) {
+    const bool wide = a.wide;
+    if (a.dtype == KDA_BF16) return wide ? fwd_v<__bf16, 8>(a) : fwd_v<__bf16, 1>(a);
+    return wide ? fwd_v<float, 4>(a) : fwd_v<float, 1>(a);
+}
+
+hipError_t launch_conv_bwd(const ConvBwdArgs& b) {
+    const bool wide = b.f.wide;
+    if (b.f.dtype == KDA_BF16) return wide ? bwd_v<__bf16, 8>(b) : bwd_v<__bf16, 1>(b);
+    return wide ? bwd_v<float, 4>(b) : bwd_v<float, 1>(b);
+}
+
+}  // namespace kda

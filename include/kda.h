@@ -392,12 +392,133 @@ int kda_chunk_fwd_noalloc(const void* q, const void* k, const void* v, const flo
 /* Bytes of the scratch array behind kda_chunk_fwd_noalloc (KDA_NOALLOC_SCRATCH_MB MiB). */
 size_t kda_noalloc_scratch_bytes(void);
 
+/*
+ * The operators around the mixer. Their conventions are those above (caller-owned device
+ * pointers, packed and dense modes, skipped and flagged slots, host-checked arguments,
+ * nothing allocated or synchronised), with these additions:
+ *   - x (and b, c, dt) may be columns of a wider tensor, such as one projection's output:
+ *     consecutive rows (tokens; row b T + t) are `*_stride` elements apart and contiguous
+ *     inside. Every other tensor is contiguous.
+ *   - dtype is KDA_BF16 or KDA_F32 for the activations; arithmetic, sums and states are fp32.
+ *   - A NaN or infinity in a token never reaches another sequence. kda_ssm_chunk_fwd may let
+ *     it reach earlier outputs of its own 64-token chunk (0 times NaN in a matrix product).
+ *
+ * Short causal depthwise convolution with bias and SiLU, ahead of the delta rule's q, k, v
+ * or the scan's x, b, c (all side by side as the D channels):
+ *     pre[t, d] = bias[d] + sum_i weight[d, i] x[t - (W-1) + i, d]
+ *     y = pre * sigmoid(pre) (activation KDA_ACT_SILU) or pre (KDA_ACT_NONE)
+ * Rows before a sequence's first token are its state, [N, W-1, D] in dtype, oldest first
+ * (zeros when initial_state is NULL); final_state receives the last W-1 rows seen and may
+ * be initial_state. A decode step is the dense mode with T = 1.
+ *   W           2, 3 or 4.   D: any.   weight [D, W], bias [D] or NULL: w_dtype.
+ * Rows that are whole 16-byte pieces at 16-byte aligned addresses move fastest; others work.
+ * In packed mode tiles are found by searching the offsets, so where some slot's offsets are
+ * broken other slots' rows may be left unwritten too.
+ */
+enum kda_activation {
+    KDA_ACT_NONE = 0,
+    KDA_ACT_SILU = 1
+};
+int kda_conv_fwd(const void* x, long long x_stride, const void* weight, const void* bias,
+                 const void* initial_state, const int32_t* cu_seqlens, int N, void* y,
+                 void* final_state, int B, int T, int D, int W, int dtype, int w_dtype,
+                 int activation, int32_t* dev_status, hipStream_t stream);
+
+/*
+ * Gradients of kda_conv_fwd (the same x, weight, bias, initial_state and options).
+ *   dy        [B, T, D] in dtype.     dfinal  [N, W-1, D] in dtype or NULL: with respect to
+ *                                     the final state.
+ *   dx        [B, T, D] in dtype.     dinitial [N, W-1, D] in dtype, or NULL.
+ *   dweight   fp32 [D, W].            dbias   fp32 [D], or NULL.
+ *   workspace at least kda_conv_bwd_workspace_bytes(...) bytes, 16-byte aligned; one call's.
+ * Rows of dx outside every sequence are not written.
+ */
+int kda_conv_bwd(const void* dy, const void* x, long long x_stride, const void* weight,
+                 const void* bias, const void* initial_state, const int32_t* cu_seqlens, int N,
+                 const void* dfinal, void* dx, float* dweight, float* dbias, void* dinitial,
+                 int B, int T, int D, int W, int dtype, int w_dtype, int activation,
+                 void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                 hipStream_t stream);
+size_t kda_conv_bwd_workspace_bytes(int B, int T, int D, int W, int N, int packed, int dtype);
+
+/*
+ * Selective state space scan: the gated delta rule's state with one decay per head and
+ * step and no erase. Per sequence n and head hv (b / c group h = hv / (HV / H)), S fp32 [K, V]:
+ *     dt' = softplus(dt + dt_bias[hv]) (dt_softplus != 0) or dt + dt_bias[hv]
+ *     S <- exp(-exp(A_log[hv]) dt') S + b_t (dt' x_t)^T
+ *     y_t = S^T c_t + D[hv] x_t
+ *   x, y       [B, T, HV, V] in dtype (y contiguous).   dt  [B, T, HV] in dt_dtype.
+ *   b, c       [B, T, H, K] in dtype.
+ *   A_log      fp32 [HV].   D, dt_bias: fp32 [HV] or NULL (zeros).
+ *   states     fp32 [N, HV, K, V]; final_state may be initial_state.
+ *   K          64 or 128.   V: a multiple of 64.
+ * x, b, c, y and the states must be 16-byte aligned, x_stride, b_stride and c_stride whole
+ * 16-byte pieces. dt' is expected >= 0 (the softplus makes it so); a step's log2 decay is
+ * taken as at least -1e5, where its exponential is 0 either way.
+ *
+ * kda_ssm_chunk_fwd is the prompt's form (chunks of 64 tokens on the matrix cores),
+ * kda_ssm_recurrent_fwd walks tokens one by one (decode, short prompts).
+ *   workspace  at least kda_ssm_chunk_fwd_workspace_bytes(...) bytes, 256-byte aligned; it
+ *              may be NULL where that is 0.
+ */
+int kda_ssm_chunk_fwd(const void* x, long long x_stride, const void* dt, long long dt_stride,
+                      const float* A_log, const void* b, long long b_stride, const void* c,
+                      long long c_stride, const float* D, const float* dt_bias,
+                      const float* initial_state, const int32_t* cu_seqlens, int N, void* y,
+                      float* final_state, int B, int T, int H, int HV, int K, int V, int dtype,
+                      int dt_dtype, int dt_softplus, void* workspace, size_t workspace_bytes,
+                      int32_t* dev_status, hipStream_t stream);
+size_t kda_ssm_chunk_fwd_workspace_bytes(int B, int T, int H, int HV, int K, int V, int N,
+                                         int packed, int dtype);
+int kda_ssm_recurrent_fwd(const void* x, long long x_stride, const void* dt, long long dt_stride,
+                          const float* A_log, const void* b, long long b_stride, const void* c,
+                          long long c_stride, const float* D, const float* dt_bias,
+                          const float* initial_state, const int32_t* cu_seqlens, int N, void* y,
+                          float* final_state, int B, int T, int H, int HV, int K, int V,
+                          int dtype, int dt_dtype, int dt_softplus, int32_t* dev_status,
+                          hipStream_t stream);
+
+/*
+ * RMS norm over the last axis with the residual's addition:
+ *     h = x + residual (x without one),  r = (mean h^2 + eps)^(-1/2),  y = h r weight
+ *   x          rows of D, x_stride elements apart; residual, h and y [rows, D] in dtype.
+ *   h          NULL, or receives h in dtype; the norm uses the fp32 sum. h may be residual,
+ *              y may be x (when x is contiguous).
+ *   rstd       NULL, or fp32 [rows] receiving r (the backward's input).
+ * kda_rmsnorm_quant_fwd leaves q uint8 [rows, D] instead of y: OCP e4m3 codes of y / s and
+ * s fp32 [rows, D / group] with s = max(max |y|, 2^-110) / 448 over the group's columns
+ * (group D: one scale a row; group 128: D a multiple of 128, and rows 16-byte aligned).
+ * A NaN in a row gives NaN codes.
+ *   D          up to 65536 (bf16) or 32768 (fp32) where rows are whole 16-byte pieces at
+ *              aligned addresses, else up to 8192.
+ */
+int kda_rmsnorm_fwd(const void* x, long long x_stride, const void* weight, const void* residual,
+                    void* y, void* h, float* rstd, long long rows, int D, float eps, int dtype,
+                    int w_dtype, hipStream_t stream);
+int kda_rmsnorm_quant_fwd(const void* x, long long x_stride, const void* weight,
+                          const void* residual, uint8_t* q, float* scales, void* h,
+                          long long rows, int D, int group, float eps, int dtype, int w_dtype,
+                          hipStream_t stream);
+
+/*
+ * Gradients of kda_rmsnorm_fwd from h and its rstd: with xh = h rstd,
+ *     dx = dh + rstd (weight dy - xh mean(weight dy xh)),  dweight = sum over rows of dy xh
+ * (the gradient of x and of residual alike). dh, or NULL for zeros, is the gradient that
+ * reaches h along the residual stream. All activations [rows, D] in dtype and contiguous,
+ * dweight fp32 [D]. dx may be dy or dh.
+ *   workspace  at least kda_rmsnorm_bwd_workspace_bytes(...) bytes, 16-byte aligned.
+ */
+int kda_rmsnorm_bwd(const void* dy, const void* h, const void* weight, const float* rstd,
+                    const void* dh, void* dx, float* dweight, long long rows, int D, int dtype,
+                    int w_dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t kda_rmsnorm_bwd_workspace_bytes(long long rows, int D, int dtype);
+
 /* Reason for the last non-KDA_OK return on this thread ("" if none). */
 const char* kda_last_error(void);
 
 /* ABI version of this header (bumped on any signature change or added entry point);
  * the library returns the KDA_ABI_VERSION it was built with. */
-#define KDA_ABI_VERSION 7
+#define KDA_ABI_VERSION 8
 int kda_abi_version(void);
 
 #ifdef __cplusplus
