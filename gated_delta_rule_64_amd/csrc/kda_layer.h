@@ -101,7 +101,7 @@ hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a);
 int norm_bwd_partials(long long rows, int D, int dtype);
 hipError_t launch_ssm_recurrent(const SsmArgs& a);
 hipError_t launch_ssm_chunk(const SsmArgs& a);
-size_t ssm_chunk_workspace(int B, int T, int HV, int K, int V, int N, bool packed, int dtype);
+size_t ssm_chunk_workspace(int B, int T, int H, int HV, int K, int V, int N, bool packed, int dtype);
 
 // out[m] (or, transposed, out[(m % D) * (M / D) + m / D]) = sum over p of part[p * M + m],
 // in the order of p
@@ -232,10 +232,10 @@ __device__ __forceinline__ float ssm_step(float raw, float bias, int softplus) {
     if (!softplus) return z;
     return z > 20.f ? z : log1pf(expf(z));
 }
-// the log2 decay of a step; bounded at -1e5, where its exponential is 0 all the same, so
-// that sums and differences of decays stay finite
+// the log2 decay of a step; bounded at -200, where its exponential is 0 all the same, so
+// that sums of decays stay finite and their differences exact enough
 __device__ __forceinline__ double ssm_log2_decay(float dt, float A_log) {
-    return fmax((double)dt * (-(double)expf(A_log) * 1.4426950408889634), -1e5);
+    return fmax((double)dt * (-(double)expf(A_log) * 1.4426950408889634), -200.0);
 }
 
 }  // namespace kda

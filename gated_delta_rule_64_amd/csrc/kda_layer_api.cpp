@@ -189,7 +189,7 @@ size_t kda_ssm_chunk_fwd_workspace_bytes(int B, int T, int H, int HV, int K, int
     if (B < 0 || T < 0 || H <= 0 || HV <= 0 || N < 0 || HV % H != 0 || (K != 64 && K != 128) || V <= 0 || V % 64 != 0 ||
         !is_dtype(dtype))
         return 0;
-    return kda::ssm_chunk_workspace(B, T, HV, K, V, packed ? N : B, packed != 0, dtype);
+    return kda::ssm_chunk_workspace(B, T, H, HV, K, V, packed ? N : B, packed != 0, dtype);
 }
 
 int kda_ssm_chunk_fwd(const void* x, long long x_stride, const void* dt, long long dt_stride, const float* A_log,
@@ -204,7 +204,7 @@ int kda_ssm_chunk_fwd(const void* x, long long x_stride, const void* dt, long lo
                           stream))
         return rc;
     if (N == 0) return KDA_OK;
-    const size_t need = kda::ssm_chunk_workspace(B, T, HV, K, V, N, cu_seqlens != nullptr, dtype);
+    const size_t need = kda::ssm_chunk_workspace(B, T, H, HV, K, V, N, cu_seqlens != nullptr, dtype);
     if (int rc = check_workspace(workspace, workspace_bytes, need, 256)) return rc;
     a.workspace = workspace;
     return launched(kda::launch_ssm_chunk(a));
