@@ -109,6 +109,16 @@ struct Steps {
     float all;            // 2^(cum_63)
 };
 
+// The bits of token `row`'s dt of head hv: widened only where they are used, so that the load
+// is not waited for before.
+__device__ __forceinline__ uint32_t load_dt_bits(const SsmArgs& a, long long row, int hv) {
+    const long long at = row * a.dt_stride + hv;
+    return a.dt_dtype == KDA_BF16 ? (uint32_t) static_cast<const uint16_t*>(a.dt)[at] : static_cast<const uint32_t*>(a.dt)[at];
+}
+__device__ __forceinline__ float dt_of_bits(const SsmArgs& a, uint32_t bits) {
+    return __uint_as_float(a.dt_dtype == KDA_BF16 ? bits << 16 : bits);
+}
+
 // One wave: lane j takes token j of `len`, whose raw dt it brings. The running sums are
 // formed in fp64: the exponents are differences of them.
 __device__ __forceinline__ void chunk_steps(float raw, int len, float A_log, float bias, int softplus, Steps* s) {
@@ -226,8 +236,7 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
             store_vec<4>(Xs + t * LDX + q, u);
         }
         if (wave == 0) {
-            const float raw = lane < cl ? load_scalar(a.dt, a.dt_dtype, (row + lane) * a.dt_stride + hv) : 0.f;
-            chunk_steps(raw, cl, A_log, bias, a.softplus, &st);
+            chunk_steps(dt_of_bits(a, load_dt_bits(a, row + min(lane, cl - 1), hv)), cl, A_log, bias, a.softplus, &st);
         }
         __syncthreads();
         if constexpr (!FIRST) {
@@ -355,9 +364,10 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
     constexpr int KT = K / 16, KS = K / 32;
     constexpr int LDK = K + GAP, LDX = SLAB + GAP;
     constexpr int NB = C * K / 8 / 256, NX = C * SLAB / 8 / 256;   // 16-byte pieces a thread
+    constexpr int RB = 256 / (K / 8), RX = 256 / (SLAB / 8);       // rows between them
     __shared__ __attribute__((aligned(16))) __bf16 Bs[C * LDK], Cs[FIRST ? 8 : C * LDK], Xs[NS][C * LDX];
     __shared__ __attribute__((aligned(16))) __bf16 Ms[FIRST ? 1 : NS][FIRST ? 8 : 6 * 64 * 8];
-    __shared__ Steps st[NS];
+    __shared__ Steps steps[2][NS];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int l16 = lane & 15, g = lane >> 4;
     if (!FIRST && blockIdx.x == 0) flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
@@ -366,6 +376,45 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
     const Work w = FIRST ? first_pass_work(tile, a, p) : second_pass_work(tile, a, p);
     if (w.len < 0) return;
     const int vs = a.V / SLAB, h = slab0 / vs / (a.HV / a.H);
+    const int begin = w.s * p.seg;
+    const int stop = w.len - begin < p.seg ? w.len : begin + p.seg;
+
+    // this thread's pieces of a chunk; past the sequence's end the last row stands in (its
+    // weights are 0 there)
+    const int tb = tid / (K / 8), tx = tid / (SLAB / 8);
+    const __bf16* bp = static_cast<const __bf16*>(a.b) + w.row0 * a.b_stride + (size_t)h * K + tid % (K / 8) * 8;
+    const __bf16* cp = static_cast<const __bf16*>(a.c) + w.row0 * a.c_stride + (size_t)h * K + tid % (K / 8) * 8;
+    const __bf16* xp = static_cast<const __bf16*>(a.x) + w.row0 * a.x_stride + (size_t)slab0 * SLAB + tid % (SLAB / 8) * 8;
+    bf16x8 rb[NB], rc[FIRST ? 1 : NB], rx[NS][NX];
+    auto fetch = [&](int p0) {
+        const int last = w.len - 1;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const long long t = min(p0 + tb + i * RB, last);
+            rb[i] = *reinterpret_cast<const bf16x8*>(bp + t * a.b_stride);
+            if constexpr (!FIRST) rc[i] = *reinterpret_cast<const bf16x8*>(cp + t * a.c_stride);
+        }
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const __bf16* at = xp + (long long)min(p0 + tx + i * RX, last) * a.x_stride;
+#pragma unroll
+            for (int q = 0; q < NS; ++q) rx[q][i] = *reinterpret_cast<const bf16x8*>(at + q * SLAB);
+        }
+    };
+    // wave q < NS forms slab q's steps, a chunk ahead, from dt it loads two chunks ahead
+    const int my_hv = (slab0 + (wave < NS ? wave : 0)) / vs;
+    const float my_A = a.A_log[my_hv], my_bias = a.dt_bias ? a.dt_bias[my_hv] : 0.f;
+    uint32_t bits = 0;
+    auto fetch_dt = [&](int p0) {
+        if (wave < NS) bits = load_dt_bits(a, w.row0 + min(p0 + lane, w.len - 1), my_hv);
+    };
+    auto form_steps = [&](int p0) {
+        if (wave < NS) chunk_steps(dt_of_bits(a, bits), w.len - p0, my_A, my_bias, a.softplus, &steps[(p0 / C) & 1][wave]);
+    };
+    if (begin < stop) {
+        fetch_dt(begin);
+        fetch(begin);
+    }
 
     f32x4 S[NS][KT];
 #pragma unroll
@@ -376,9 +425,6 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
     float skip[NS];
 #pragma unroll
     for (int q = 0; q < NS; ++q) skip[q] = a.D ? a.D[(slab0 + q) / vs] : 0.f;
-    // wave q < NS forms slab q's steps
-    const int my_hv = (slab0 + (wave < NS ? wave : 0)) / vs;
-    const float my_A = a.A_log[my_hv], my_bias = a.dt_bias ? a.dt_bias[my_hv] : 0.f;
     double total = 0.0;
     if constexpr (!FIRST) {
         // the halves of M's fragments above the diagonal: token blocks 1 of I = 0, 3 of I = 2
@@ -389,53 +435,32 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
                 *reinterpret_cast<bf16x4*>(Ms[q] + (m_frag(2, 1) * 64 + lane) * 8 + 4) = bf16x4{};
             }
     }
+    if (begin < stop) {
+        form_steps(begin);
+        if (begin + C < stop) fetch_dt(begin + C);
+    }
+    const long long y_row = (long long)p.slabs * SLAB;
+    __bf16* yp = static_cast<__bf16*>(a.y) + (w.row0 + begin + l16) * y_row + slab0 * SLAB + 16 * wave + 4 * g;
 
-    const __bf16* bp = static_cast<const __bf16*>(a.b) + (size_t)h * K;
-    const __bf16* cp = static_cast<const __bf16*>(a.c) + (size_t)h * K;
-    const __bf16* xp = static_cast<const __bf16*>(a.x) + (size_t)slab0 * SLAB;
-    bf16x8 rb[NB], rc[FIRST ? 1 : NB], rx[NS][NX];
-    float rdt = 0.f;
-    auto fetch = [&](int p0) {
+    for (int p0 = begin; p0 < stop; p0 += C, yp += C * y_row) {
         const int cl = w.len - p0 < C ? w.len - p0 : C;
-        const long long row = w.row0 + p0;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int piece = i * 256 + tid, t = piece / (K / 8), k = piece % (K / 8) * 8;
-            rb[i] = t < cl ? *reinterpret_cast<const bf16x8*>(bp + (row + t) * a.b_stride + k) : bf16x8{};
-            if constexpr (!FIRST) rc[i] = t < cl ? *reinterpret_cast<const bf16x8*>(cp + (row + t) * a.c_stride + k) : bf16x8{};
-        }
-#pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const int piece = i * 256 + tid, t = piece / (SLAB / 8), k = piece % (SLAB / 8) * 8;
-#pragma unroll
-            for (int q = 0; q < NS; ++q)
-                rx[q][i] = t < cl ? *reinterpret_cast<const bf16x8*>(xp + (row + t) * a.x_stride + q * SLAB + k) : bf16x8{};
-        }
-        if (wave < NS) rdt = lane < cl ? load_scalar(a.dt, a.dt_dtype, (row + lane) * a.dt_stride + my_hv) : 0.f;
-    };
-
-    const int begin = w.s * p.seg;
-    const int stop = w.len - begin < p.seg ? w.len : begin + p.seg;
-    if (begin < stop) fetch(begin);
-    for (int p0 = begin; p0 < stop; p0 += C) {
-        const int cl = w.len - p0 < C ? w.len - p0 : C;
-        const long long row = w.row0 + p0;
+        const Steps* st = steps[(p0 / C) & 1];
         lds_barrier();   // the last chunk's readers are done
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int piece = i * 256 + tid, t = piece / (K / 8), k = piece % (K / 8) * 8;
-            *reinterpret_cast<bf16x8*>(Bs + t * LDK + k) = rb[i];
-            if constexpr (!FIRST) *reinterpret_cast<bf16x8*>(Cs + t * LDK + k) = rc[i];
+            *reinterpret_cast<bf16x8*>(Bs + (tb + i * RB) * LDK + tid % (K / 8) * 8) = rb[i];
+            if constexpr (!FIRST) *reinterpret_cast<bf16x8*>(Cs + (tb + i * RB) * LDK + tid % (K / 8) * 8) = rc[i];
         }
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const int piece = i * 256 + tid, t = piece / (SLAB / 8), k = piece % (SLAB / 8) * 8;
+        for (int i = 0; i < NX; ++i)
 #pragma unroll
-            for (int q = 0; q < NS; ++q) *reinterpret_cast<bf16x8*>(Xs[q] + t * LDX + k) = rx[q][i];
-        }
-        if (wave < NS) chunk_steps(rdt, cl, my_A, my_bias, a.softplus, &st[wave]);
+            for (int q = 0; q < NS; ++q) *reinterpret_cast<bf16x8*>(Xs[q] + (tx + i * RX) * LDX + tid % (SLAB / 8) * 8) = rx[q][i];
         lds_barrier();
-        if (p0 + C < stop) fetch(p0 + C);   // in flight while this chunk is worked on
+        if (p0 + C < stop) {   // in flight while this chunk is worked on
+            fetch(p0 + C);
+            form_steps(p0 + C);
+            if (p0 + 2 * C < stop) fetch_dt(p0 + 2 * C);
+        }
 
         if constexpr (!FIRST) {
             // M^T: wave w forms token rows J <= w of token columns 16 w ..
@@ -459,7 +484,7 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float e = exp2_fast((hi - hj[r]) + (lo - lj[r])) * dj[r];
-                        m[r] = (__bf16)(j0 + r <= i ? acc[r] * e : 0.f);
+                        m[r] = (__bf16)(J < wave || j0 + r <= i ? acc[r] * e : 0.f);
                     }
                     *reinterpret_cast<bf16x4*>(Ms[q] + (m_frag(wave, J >> 1) * 64 + lane) * 8 + 4 * (J & 1)) = m;
                 }
@@ -502,19 +527,18 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
 #pragma unroll
                     for (int s = 0; s <= (I >> 1); ++s)
                         acc = mma32(xf[q][s], *reinterpret_cast<const bf16x8*>(Ms[q] + (m_frag(I, s) * 64 + lane) * 8), acc);
-                    if (i < cl) {   // columns 16 wave + 4 g .. +3 of token i
-                        const int col = 16 * wave + 4 * g;
-                        const bf16x4 xi = *reinterpret_cast<const bf16x4*>(Xs[q] + i * LDX + col);
-                        bf16x4 out;
+                    // columns 16 wave + 4 g .. +3 of token i
+                    const bf16x4 xi = *reinterpret_cast<const bf16x4*>(Xs[q] + i * LDX + 16 * wave + 4 * g);
+                    bf16x4 out;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) out[r] = (__bf16)fmaf(skip[q], (float)xi[r], acc[r]);
-                        *reinterpret_cast<bf16x4*>(static_cast<__bf16*>(a.y) + ((row + i) * p.slabs + slab0 + q) * (long long)SLAB + col) = out;
-                    }
+                    for (int r = 0; r < 4; ++r) out[r] = (__bf16)fmaf(skip[q], (float)xi[r], acc[r]);
+                    if (i < cl) *reinterpret_cast<bf16x4*>(yp + 16 * I * y_row + q * SLAB) = out;
                 }
+                __builtin_amdgcn_sched_barrier(0);   // keeps the four blocks' operands from being live at once
             }
         }
         // the state at the chunk's end
-        bf16x8 xw[NS][2][3];
+        if (FIRST && wave < NS) total += st[wave].end;
 #pragma unroll
         for (int q = 0; q < NS; ++q) {
             const float all = st[q].all;
@@ -522,30 +546,36 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) S[q][t][r] *= all;
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = (float)xf[q][s][e] * st[q].grow[32 * s + 16 * (e >> 2) + 4 * g + (e & 3)];
-                    const __bf16 v0 = (__bf16)v;
-                    const float r1 = v - (float)v0;
-                    const __bf16 v1 = (__bf16)r1;
-                    xw[q][s][0][e] = v0;
-                    xw[q][s][1][e] = v1;
-                    xw[q][s][2][e] = (__bf16)(r1 - (float)v1);
-                }
         }
-        if (FIRST && wave < NS) total += st[wave].end;
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+        for (int s = 0; s < 2; ++s) {
+            bf16x8 xw[NS][3];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int q = 0; q < NS; ++q)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const f32x4 grow = *reinterpret_cast<const f32x4*>(st[q].grow + 32 * s + 16 * hf + 4 * g);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int e = 4 * hf + r;
+                        const float v = (float)xf[q][s][e] * grow[r];
+                        const __bf16 v0 = (__bf16)v;
+                        const float r1 = v - (float)v0;
+                        const __bf16 v1 = (__bf16)r1;
+                        xw[q][0][e] = v0;
+                        xw[q][1][e] = v1;
+                        xw[q][2][e] = (__bf16)(r1 - (float)v1);
+                    }
+                }
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
                 const bf16x8 bt = join(read_col4<LDK>(Bs, 2 * s, 16 * t), read_col4<LDK>(Bs, 2 * s + 1, 16 * t));
 #pragma unroll
                 for (int q = 0; q < NS; ++q)
 #pragma unroll
-                    for (int u = 2; u >= 0; --u) S[q][t] = mma32(bt, xw[q][s][u], S[q][t]);
+                    for (int u = 2; u >= 0; --u) S[q][t] = mma32(bt, xw[q][u], S[q][t]);
             }
+        }
     }
     if constexpr (FIRST) {
 #pragma unroll
