@@ -32,11 +32,11 @@ int check_sequences(const int32_t* cu, int N, int B, int T) {
     return KDA_OK;
 }
 
-int check_stride(const char* name, long long stride, long long width) {
+int check_stride(const char* name, long long stride, long long width, long long most = 1LL << 31) {
     if (stride < width)
         return set_error(KDA_ERR_SHAPE, "%s=%lld is less than a row's %lld elements", name, stride, width);
-    if (stride > (1LL << 31))
-        return set_error(KDA_ERR_SHAPE, "%s=%lld exceeds 2^31", name, stride);
+    if (stride > most)
+        return set_error(KDA_ERR_SHAPE, "%s=%lld exceeds %lld", name, stride, most);
     return KDA_OK;
 }
 
@@ -90,14 +90,14 @@ int ssm_args(kda::SsmArgs* a, const void* x, long long x_stride, const void* dt,
     if (HV % H != 0) return set_error(KDA_ERR_SHAPE, "HV=%d must be a multiple of H=%d", HV, H);
     if (K != 64 && K != 128) return set_error(KDA_ERR_UNSUPPORTED, "K must be 64 or 128, got %d", K);
     if (V <= 0 || V % 64 != 0) return set_error(KDA_ERR_UNSUPPORTED, "V must be a multiple of 64, got %d", V);
-    if ((long long)HV * V > (1LL << 28) || (long long)HV * K > (1LL << 28))
+    if ((long long)HV * V >= (1LL << 24) || (long long)HV * K >= (1LL << 24))
         return set_error(KDA_ERR_SHAPE, "a row of HV=%d heads of K=%d, V=%d is too wide", HV, K, V);
     if ((long long)N * HV > 0x7fffffffLL / (V / 32))
         return set_error(KDA_ERR_SHAPE, "N*HV=%lld too large", (long long)N * HV);
-    if (int rc = check_stride("x_stride", x_stride, (long long)HV * V)) return rc;
-    if (int rc = check_stride("dt_stride", dt_stride, HV)) return rc;
-    if (int rc = check_stride("b_stride", b_stride, (long long)H * K)) return rc;
-    if (int rc = check_stride("c_stride", c_stride, (long long)H * K)) return rc;
+    if (int rc = check_stride("x_stride", x_stride, (long long)HV * V, (1 << 24) - 1)) return rc;
+    if (int rc = check_stride("dt_stride", dt_stride, HV, (1 << 24) - 1)) return rc;
+    if (int rc = check_stride("b_stride", b_stride, (long long)H * K, (1 << 24) - 1)) return rc;
+    if (int rc = check_stride("c_stride", c_stride, (long long)H * K, (1 << 24) - 1)) return rc;
     const int vec = dtype == KDA_BF16 ? 8 : 4;
     if (x_stride % vec || b_stride % vec || c_stride % vec)
         return set_error(KDA_ERR_SHAPE, "x_stride, b_stride and c_stride must be multiples of %d (16 bytes)", vec);

@@ -43,6 +43,7 @@ struct Plan {
     float* starts;        // the same size: initial states of cut sequences, where final_state
                           // is initial_state and would be overwritten before it is read
     float* decay;         // [slots][slabs]
+    const float* steps;   // [3][HV][rows], see ssm_steps_kernel
 };
 
 struct Work {
@@ -100,51 +101,78 @@ __device__ __forceinline__ Work first_pass_work(long long slot, const SsmArgs& a
 }
 
 // Per-chunk scalars of one head in LDS
-struct Steps {
+struct alignas(16) Steps {
     float dt[C];
     float hi[C], lo[C];   // running sums of the log2 decay, as hi + lo
     float grow[C];        // 2^(cum_63 - cum_j) dt'_j
     float fall[C];        // 2^(cum_i)
-    double end;           // cum_63
     float all;            // 2^(cum_63)
 };
 
-// The bits of token `row`'s dt of head hv: widened only where they are used, so that the load
-// is not waited for before.
-__device__ __forceinline__ uint32_t load_dt_bits(const SsmArgs& a, long long row, int hv) {
-    const long long at = row * a.dt_stride + hv;
-    return a.dt_dtype == KDA_BF16 ? (uint32_t) static_cast<const uint16_t*>(a.dt)[at] : static_cast<const uint32_t*>(a.dt)[at];
-}
-__device__ __forceinline__ float dt_of_bits(const SsmArgs& a, uint32_t bits) {
-    return __uint_as_float(a.dt_dtype == KDA_BF16 ? bits << 16 : bits);
+// dt' and the running sums of the log2 decay inside each chunk, for every row and head:
+// steps[0], [1], [2] are dt', hi and lo as [HV][rows] (the sums are formed in fp64, since
+// the exponents are differences of them, and kept as hi + lo). One block: a chunk of a
+// sequence and 8 heads; a wave takes a head, its lane a token. Formed once instead of in
+// every block that walks the chunk, where one wave's transcendentals and 64-bit prefix sums
+// held up the others (first pass of 32768 x 64 heads: 157 us with, 112 without them).
+constexpr int STEP_HEADS = 8;
+__global__ __launch_bounds__(256) void ssm_steps_kernel(const SsmArgs a, float* steps, int per, int hblocks) {
+    __shared__ float raw[C][STEP_HEADS + 1];
+    if (blockIdx.x == 0) flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
+    const int h0 = (int)(blockIdx.x % hblocks) * STEP_HEADS;
+    const SeqTile s = seq_tile(blockIdx.x / hblocks, a.cu_seqlens, a.N, a.T, C, per);
+    const int cl = min(s.len - s.pos, C);
+    if (cl <= 0) return;
+    const long long row = s.row0 + s.pos, rows = (long long)a.B * a.T;
+    for (int i = threadIdx.x; i < C * STEP_HEADS; i += 256) {
+        const int t = i / STEP_HEADS, hv = i % STEP_HEADS;
+        if (t < cl && h0 + hv < a.HV) raw[t][hv] = load_scalar(a.dt, a.dt_dtype, (row + t) * a.dt_stride + h0 + hv);
+    }
+    __syncthreads();
+    const int j = threadIdx.x & 63;
+    for (int k = threadIdx.x >> 6; k < STEP_HEADS && h0 + k < a.HV; k += 4) {
+        const int hv = h0 + k;
+        float dt = 0.f;
+        double cum = 0.0;
+        if (j < cl) {
+            dt = ssm_step(raw[j][k], a.dt_bias ? a.dt_bias[hv] : 0.f, a.softplus);
+            cum = ssm_log2_decay(dt, a.A_log[hv]);
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const double up = __shfl_up(cum, o, 64);
+            if (j >= o) cum += up;
+        }
+        if (j < cl) {
+            const float hi = (float)cum;
+            const long long at = (long long)hv * rows + row + j;
+            steps[at] = dt;
+            steps[at + a.HV * rows] = hi;
+            steps[at + 2 * a.HV * rows] = (float)(cum - (double)hi);
+        }
+    }
 }
 
-// One wave: lane j takes token j of `len`, whose raw dt it brings. The running sums are
-// formed in fp64: the exponents are differences of them.
-__device__ __forceinline__ void chunk_steps(float raw, int len, float A_log, float bias, int softplus, Steps* s) {
+// One wave's token of a chunk: what the steps kernel left for it, and from that the
+// chunk's scalars. Tokens past the chunk's `cl` take its last one with a weight of 0.
+struct Step { float dt, hi, lo; };
+__device__ __forceinline__ Step load_step(const SsmArgs& a, const Plan& p, long long row, int cl, int hv) {
     const int j = threadIdx.x & 63;
-    float dt = 0.f;
-    double cum = 0.0;
-    if (j < len) {
-        dt = ssm_step(raw, bias, softplus);
-        cum = ssm_log2_decay(dt, A_log);
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o *= 2) {
-        const double up = __shfl_up(cum, o, 64);
-        if (j >= o) cum += up;
-    }
-    const double end = __shfl(cum, 63, 64);
+    const long long rows = (long long)a.B * a.T, at = (long long)hv * rows + row + min(j, cl - 1);
+    return Step{p.steps[at], p.steps[at + a.HV * rows], p.steps[at + 2 * a.HV * rows]};
+}
+__device__ __forceinline__ double place_steps(const Step& v, int cl, Steps* s) {
+    const int j = threadIdx.x & 63;
+    const float dt = j < cl ? v.dt : 0.f;
+    const float eh = __shfl(v.hi, 63, 64), el = __shfl(v.lo, 63, 64);
+    const float fall = exp2_fast(v.hi);
     s->dt[j] = dt;
-    const float hi = (float)cum;
-    s->hi[j] = hi;
-    s->lo[j] = (float)(cum - (double)hi);
-    s->grow[j] = exp2_fast((float)(end - cum)) * dt;
-    s->fall[j] = exp2_fast(hi);
-    if (j == 63) {
-        s->end = cum;
-        s->all = exp2_fast(hi);
-    }
+    s->hi[j] = v.hi;
+    s->lo[j] = v.lo;
+    s->grow[j] = exp2_fast((eh - v.hi) + (el - v.lo)) * dt;
+    s->fall[j] = fall;
+    if (j == 63) s->all = fall;
+    return (double)eh + (double)el;
 }
 
 // The state a segment starts from, in accumulators, and where one goes: [K][V] with this
@@ -178,7 +206,11 @@ template <int KT> __device__ __forceinline__ void store_slot(const f32x4 (&S)[KT
     for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4*>(at + t * 1024) = S[t];
 }
 template <int KT> __device__ __forceinline__ void store_final(const f32x4 (&S)[KT], const SsmArgs& a, int n, int slab) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
+    int tid = threadIdx.x;
+    // the addresses are those load_start forms: keep the compiler from holding them in
+    // registers (64 of them) all through the walk
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
     const int vs = a.V / SLAB, hv = slab / vs;
     float* hT = a.final_state + ((size_t)n * a.HV + hv) * (size_t)(KT * 16) * a.V + (slab % vs) * SLAB + 16 * wave + l16;
 #pragma unroll
@@ -200,7 +232,6 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
     __shared__ Steps st;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int l16 = lane & 15, g = lane >> 4;
-    if (!FIRST && blockIdx.x == 0) flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
     const int slab = (int)(blockIdx.x % p.slabs);
     const long long tile = blockIdx.x / p.slabs;
     const Work w = FIRST ? first_pass_work(tile, a, p) : second_pass_work(tile, a, p);
@@ -209,8 +240,6 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
     f32x4 S[KT];
     load_start(S, a, p, w, slab, FIRST);
     if (FIRST && w.s == 0 && p.starts) store_slot(S, p.starts, p, w.slot0, slab);
-    const float A_log = a.A_log[hv];
-    const float bias = a.dt_bias ? a.dt_bias[hv] : 0.f;
     const float skip = a.D ? a.D[hv] : 0.f;
     double total = 0.0;
 
@@ -235,9 +264,7 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
             if (t < cl) load_vec<4>(static_cast<const float*>(a.x) + (row + t) * a.x_stride + (size_t)slab * SLAB + q, u);
             store_vec<4>(Xs + t * LDX + q, u);
         }
-        if (wave == 0) {
-            chunk_steps(dt_of_bits(a, load_dt_bits(a, row + min(lane, cl - 1), hv)), cl, A_log, bias, a.softplus, &st);
-        }
+        if (wave == 0) total += place_steps(load_step(a, p, row, cl, hv), cl, &st);
         __syncthreads();
         if constexpr (!FIRST) {
             // M^T: wave w forms rows J <= w of token column block w
@@ -303,7 +330,6 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
         }
         // the state at the chunk's end
         const float all = st.all;
-        if (FIRST) total += st.end;
 #pragma unroll
         for (int J = 0; J < 4; ++J)
 #pragma unroll
@@ -336,23 +362,41 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
 //     update is three products.
 //   * operands whose contraction runs over tokens (x and b down a column) are read from LDS
 //     transposed (ds_read_b64_tr_b16: four consecutive rows of a column a lane).
-// Rows in LDS are 32 bytes longer than their data, so that both the row-wise 8-byte operand
-// reads and the transposed ones (16 rows x 32 bytes a wave) spread over all banks.
+// Rows in LDS are 32 bytes longer than their data, and every eight rows begin 16 bytes
+// later: the transposed reads' half waves (8 rows x 32 bytes) and the row-wise 8-byte operand
+// reads' (16 rows x 16 bytes) then both meet every bank once.
 // ---------------------------------------------------------------------------------
 constexpr int GAP = 16;   // elements
+template <int LD> __device__ __forceinline__ constexpr int row_at(int r) { return r * LD + 8 * (r >> 3); }
 
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
 // four consecutive rows (tokens 16 J + 4 g ..) of column c0 + l % 16 of a [C][LD] tile
 template <int LD> __device__ __forceinline__ bf16x4 read_col4(const __bf16* t, int J, int c0) {
     const int lane = threadIdx.x & 63;
-    const __bf16* at = t + (16 * J + (lane >> 2)) * LD + c0 + 4 * (lane & 3);
+    const __bf16* at = t + (row_at<LD>(lane >> 2) + 4 * (lane & 3)) + (row_at<LD>(16 * J) + c0);
     return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at)));
 }
 __device__ __forceinline__ bf16x8 join(bf16x4 u, bf16x4 v) { return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7); }
 // a row's 32 elements of step s, in accumulator order: 4 g .. +3 of both halves
 __device__ __forceinline__ bf16x8 read_row(const __bf16* row, int s, int g) {
     return join(*reinterpret_cast<const bf16x4*>(row + 32 * s + 4 * g), *reinterpret_cast<const bf16x4*>(row + 32 * s + 16 + 4 * g));
+}
+// elements e and e + 1 of x times their weights, each cut into three bf16 whose sum is the
+// fp32 product exactly (8 + 8 + 8 bits, by truncation)
+__device__ __forceinline__ void split3(bf16x8 x, int e, float w0, float w1, bf16x8 (&out)[3]) {
+    const float v0 = (float)x[e] * w0, v1 = (float)x[e + 1] * w1;
+    uint32_t b0 = __float_as_uint(v0), b1 = __float_as_uint(v1);
+#pragma unroll
+    for (int u = 0; u < 3; ++u) {
+        const bf16x2 top = __builtin_bit_cast(bf16x2, __builtin_amdgcn_perm(b1, b0, 0x07060302u));
+        out[u][e] = top[0];
+        out[u][e + 1] = top[1];
+        if (u < 2) {
+            b0 = __float_as_uint(__uint_as_float(b0) - __uint_as_float(b0 & 0xffff0000u));
+            b1 = __float_as_uint(__uint_as_float(b1) - __uint_as_float(b1 & 0xffff0000u));
+        }
+    }
 }
 __device__ __forceinline__ f32x4 mma32(bf16x8 a, bf16x8 b, f32x4 c) { return Mma<__bf16>::mma(a, b, c); }
 
@@ -365,12 +409,11 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
     constexpr int LDK = K + GAP, LDX = SLAB + GAP;
     constexpr int NB = C * K / 8 / 256, NX = C * SLAB / 8 / 256;   // 16-byte pieces a thread
     constexpr int RB = 256 / (K / 8), RX = 256 / (SLAB / 8);       // rows between them
-    __shared__ __attribute__((aligned(16))) __bf16 Bs[C * LDK], Cs[FIRST ? 8 : C * LDK], Xs[NS][C * LDX];
+    __shared__ __attribute__((aligned(16))) __bf16 Bs[row_at<LDK>(C)], Cs[FIRST ? 8 : row_at<LDK>(C)], Xs[NS][row_at<LDX>(C)];
     __shared__ __attribute__((aligned(16))) __bf16 Ms[FIRST ? 1 : NS][FIRST ? 8 : 6 * 64 * 8];
     __shared__ Steps steps[2][NS];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int l16 = lane & 15, g = lane >> 4;
-    if (!FIRST && blockIdx.x == 0) flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
     const int slab0 = (int)(blockIdx.x % p.units) * NS;
     const long long tile = blockIdx.x / p.units;
     const Work w = FIRST ? first_pass_work(tile, a, p) : second_pass_work(tile, a, p);
@@ -379,40 +422,51 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
     const int begin = w.s * p.seg;
     const int stop = w.len - begin < p.seg ? w.len : begin + p.seg;
 
-    // this thread's pieces of a chunk; past the sequence's end the last row stands in (its
-    // weights are 0 there)
+    // this thread's pieces of a chunk, as 32-bit offsets from the chunk's row (a stride is at
+    // most 2^24); past the sequence's end the last row stands in (its weights are 0 there)
     const int tb = tid / (K / 8), tx = tid / (SLAB / 8);
-    const __bf16* bp = static_cast<const __bf16*>(a.b) + w.row0 * a.b_stride + (size_t)h * K + tid % (K / 8) * 8;
-    const __bf16* cp = static_cast<const __bf16*>(a.c) + w.row0 * a.c_stride + (size_t)h * K + tid % (K / 8) * 8;
-    const __bf16* xp = static_cast<const __bf16*>(a.x) + w.row0 * a.x_stride + (size_t)slab0 * SLAB + tid % (SLAB / 8) * 8;
+    const __bf16* bp = static_cast<const __bf16*>(a.b) + w.row0 * a.b_stride + (size_t)h * K;
+    const __bf16* cp = static_cast<const __bf16*>(a.c) + w.row0 * a.c_stride + (size_t)h * K;
+    const __bf16* xp = static_cast<const __bf16*>(a.x) + w.row0 * a.x_stride + (size_t)slab0 * SLAB;
+    const unsigned kb = tid % (K / 8) * 8, kx = tid % (SLAB / 8) * 8;
+    // where they go in LDS, and this lane's place in a row-wise operand (rows 16 i, RB i and
+    // RX i are whole groups of eight, so their offsets add)
+    const int putk = row_at<LDK>(tb) + kb, putx = row_at<LDX>(tx) + kx;
+    const int rowk = row_at<LDK>(l16) + 4 * g, rowx = row_at<LDX>(l16) + 16 * wave + 4 * g;
     bf16x8 rb[NB], rc[FIRST ? 1 : NB], rx[NS][NX];
+    auto piece = [](const __bf16* base, unsigned bytes) {
+        return *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(base) + bytes);
+    };
     auto fetch = [&](int p0) {
-        const int last = w.len - 1;
+        const unsigned last = min(w.len - p0, C) - 1;
+        const __bf16* bc = bp + p0 * a.b_stride;
+        const __bf16* cc = cp + p0 * a.c_stride;
+        const __bf16* xc = xp + p0 * a.x_stride;
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const long long t = min(p0 + tb + i * RB, last);
-            rb[i] = *reinterpret_cast<const bf16x8*>(bp + t * a.b_stride);
-            if constexpr (!FIRST) rc[i] = *reinterpret_cast<const bf16x8*>(cp + t * a.c_stride);
+            const unsigned t = min((unsigned)(tb + i * RB), last);
+            rb[i] = piece(bc, (__umul24(t, (unsigned)a.b_stride) + kb) * 2);
+            if constexpr (!FIRST) rc[i] = piece(cc, (__umul24(t, (unsigned)a.c_stride) + kb) * 2);
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i) {
-            const __bf16* at = xp + (long long)min(p0 + tx + i * RX, last) * a.x_stride;
+            const unsigned at = __umul24(min((unsigned)(tx + i * RX), last), (unsigned)a.x_stride) + kx;
 #pragma unroll
-            for (int q = 0; q < NS; ++q) rx[q][i] = *reinterpret_cast<const bf16x8*>(at + q * SLAB);
+            for (int q = 0; q < NS; ++q) rx[q][i] = piece(xc + q * SLAB, at * 2);
         }
     };
-    // wave q < NS forms slab q's steps, a chunk ahead, from dt it loads two chunks ahead
+    // wave q < NS places slab q's steps, a chunk ahead, from what it loads two chunks ahead
     const int my_hv = (slab0 + (wave < NS ? wave : 0)) / vs;
-    const float my_A = a.A_log[my_hv], my_bias = a.dt_bias ? a.dt_bias[my_hv] : 0.f;
-    uint32_t bits = 0;
-    auto fetch_dt = [&](int p0) {
-        if (wave < NS) bits = load_dt_bits(a, w.row0 + min(p0 + lane, w.len - 1), my_hv);
+    Step ahead{0.f, 0.f, 0.f};
+    double total = 0.0;
+    auto fetch_steps = [&](int p0) {
+        if (wave < NS) ahead = load_step(a, p, w.row0 + p0, min(w.len - p0, C), my_hv);
     };
     auto form_steps = [&](int p0) {
-        if (wave < NS) chunk_steps(dt_of_bits(a, bits), w.len - p0, my_A, my_bias, a.softplus, &steps[(p0 / C) & 1][wave]);
+        if (wave < NS) total += place_steps(ahead, min(w.len - p0, C), &steps[(p0 / C) & 1][wave]);
     };
     if (begin < stop) {
-        fetch_dt(begin);
+        fetch_steps(begin);
         fetch(begin);
     }
 
@@ -425,7 +479,6 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
     float skip[NS];
 #pragma unroll
     for (int q = 0; q < NS; ++q) skip[q] = a.D ? a.D[(slab0 + q) / vs] : 0.f;
-    double total = 0.0;
     if constexpr (!FIRST) {
         // the halves of M's fragments above the diagonal: token blocks 1 of I = 0, 3 of I = 2
         if (wave == 0)
@@ -437,29 +490,30 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
     }
     if (begin < stop) {
         form_steps(begin);
-        if (begin + C < stop) fetch_dt(begin + C);
+        if (begin + C < stop) fetch_steps(begin + C);
     }
-    const long long y_row = (long long)p.slabs * SLAB;
-    __bf16* yp = static_cast<__bf16*>(a.y) + (w.row0 + begin + l16) * y_row + slab0 * SLAB + 16 * wave + 4 * g;
+    const unsigned y_row = p.slabs * SLAB;
+    const unsigned y_at = l16 * y_row + 16 * wave + 4 * g;
+    __bf16* yp = static_cast<__bf16*>(a.y) + (w.row0 + begin) * (long long)y_row + slab0 * SLAB;
 
-    for (int p0 = begin; p0 < stop; p0 += C, yp += C * y_row) {
+    for (int p0 = begin; p0 < stop; p0 += C, yp += C * (long long)y_row) {
         const int cl = w.len - p0 < C ? w.len - p0 : C;
         const Steps* st = steps[(p0 / C) & 1];
         lds_barrier();   // the last chunk's readers are done
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            *reinterpret_cast<bf16x8*>(Bs + (tb + i * RB) * LDK + tid % (K / 8) * 8) = rb[i];
-            if constexpr (!FIRST) *reinterpret_cast<bf16x8*>(Cs + (tb + i * RB) * LDK + tid % (K / 8) * 8) = rc[i];
+            *reinterpret_cast<bf16x8*>(Bs + putk + row_at<LDK>(i * RB)) = rb[i];
+            if constexpr (!FIRST) *reinterpret_cast<bf16x8*>(Cs + putk + row_at<LDK>(i * RB)) = rc[i];
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i)
 #pragma unroll
-            for (int q = 0; q < NS; ++q) *reinterpret_cast<bf16x8*>(Xs[q] + (tx + i * RX) * LDX + tid % (SLAB / 8) * 8) = rx[q][i];
+            for (int q = 0; q < NS; ++q) *reinterpret_cast<bf16x8*>(Xs[q] + putx + row_at<LDX>(i * RX)) = rx[q][i];
         lds_barrier();
         if (p0 + C < stop) {   // in flight while this chunk is worked on
             fetch(p0 + C);
             form_steps(p0 + C);
-            if (p0 + 2 * C < stop) fetch_dt(p0 + 2 * C);
+            if (p0 + 2 * C < stop) fetch_steps(p0 + 2 * C);
         }
 
         if constexpr (!FIRST) {
@@ -467,13 +521,13 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
             bf16x8 cf[KS];
             const int i = 16 * wave + l16;
 #pragma unroll
-            for (int s = 0; s < KS; ++s) cf[s] = read_row(Cs + i * LDK, s, g);
+            for (int s = 0; s < KS; ++s) cf[s] = read_row(Cs + rowk + row_at<LDK>(16) * wave, s, 0);
 #pragma unroll
             for (int J = 0; J < 4; ++J) {
                 if (J > wave) break;
                 f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) acc = mma32(read_row(Bs + (16 * J + l16) * LDK, s, g), cf[s], acc);
+                for (int s = 0; s < KS; ++s) acc = mma32(read_row(Bs + rowk + row_at<LDK>(16 * J), s, 0), cf[s], acc);
                 const int j0 = 16 * J + 4 * g;
 #pragma unroll
                 for (int q = 0; q < NS; ++q) {
@@ -498,6 +552,7 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
             for (int s = 0; s < 2; ++s)
                 xf[q][s] = join(read_col4<LDX>(Xs[q], 2 * s, 16 * wave), read_col4<LDX>(Xs[q], 2 * s + 1, 16 * wave));
         if constexpr (!FIRST) {
+            lds_barrier();
             bf16x8 sf[NS][KS];
 #pragma unroll
             for (int q = 0; q < NS; ++q)
@@ -508,37 +563,46 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
                         sf[q][s][r] = (__bf16)S[q][2 * s][r];
                         sf[q][s][4 + r] = (__bf16)S[q][2 * s + 1][r];
                     }
-            lds_barrier();
+            // two blocks of tokens at a time, so that their chains of products interleave
 #pragma unroll
-            for (int I = 0; I < 4; ++I) {
+            for (int I = 0; I < 4; I += 2) {
                 if (16 * I >= cl) break;
-                const int i = 16 * I + l16;
-                bf16x8 cf[KS];
+                f32x4 acc[NS][2] = {};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) cf[s] = read_row(Cs + i * LDK, s, g);
+                for (int s = 0; s < KS; ++s)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const bf16x8 cf = read_row(Cs + rowk + row_at<LDK>(16 * (I + k)), s, 0);
+#pragma unroll
+                        for (int q = 0; q < NS; ++q) acc[q][k] = mma32(sf[q][s], cf, acc[q][k]);
+                    }
 #pragma unroll
                 for (int q = 0; q < NS; ++q) {
-                    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int s = 0; s < KS; ++s) acc = mma32(sf[q][s], cf[s], acc);
-                    const float f = st[q].fall[i];
+                    for (int k = 0; k < 2; ++k) {
+                        const float f = st[q].fall[16 * (I + k) + l16];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[r] *= f;
+                        for (int r = 0; r < 4; ++r) acc[q][k][r] *= f;
+                    }
 #pragma unroll
                     for (int s = 0; s <= (I >> 1); ++s)
-                        acc = mma32(xf[q][s], *reinterpret_cast<const bf16x8*>(Ms[q] + (m_frag(I, s) * 64 + lane) * 8), acc);
-                    // columns 16 wave + 4 g .. +3 of token i
-                    const bf16x4 xi = *reinterpret_cast<const bf16x4*>(Xs[q] + i * LDX + 16 * wave + 4 * g);
-                    bf16x4 out;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) out[r] = (__bf16)fmaf(skip[q], (float)xi[r], acc[r]);
-                    if (i < cl) *reinterpret_cast<bf16x4*>(yp + 16 * I * y_row + q * SLAB) = out;
+                        for (int k = 0; k < 2; ++k)
+                            acc[q][k] = mma32(xf[q][s], *reinterpret_cast<const bf16x8*>(Ms[q] + (m_frag(I + k, s) * 64 + lane) * 8), acc[q][k]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // columns 16 wave + 4 g .. +3 of token i
+                        const int i = 16 * (I + k) + l16;
+                        const bf16x4 xi = *reinterpret_cast<const bf16x4*>(Xs[q] + rowx + row_at<LDX>(16 * (I + k)));
+                        bf16x4 out;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) out[r] = (__bf16)fmaf(skip[q], (float)xi[r], acc[q][k][r]);
+                        if (i < cl) *reinterpret_cast<bf16x4*>(reinterpret_cast<char*>(yp + q * SLAB) + (y_at + 16 * (I + k) * y_row) * 2) = out;
+                    }
                 }
-                __builtin_amdgcn_sched_barrier(0);   // keeps the four blocks' operands from being live at once
             }
         }
         // the state at the chunk's end
-        if (FIRST && wave < NS) total += st[wave].end;
 #pragma unroll
         for (int q = 0; q < NS; ++q) {
             const float all = st[q].all;
@@ -556,16 +620,7 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
                 for (int hf = 0; hf < 2; ++hf) {
                     const f32x4 grow = *reinterpret_cast<const f32x4*>(st[q].grow + 32 * s + 16 * hf + 4 * g);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int e = 4 * hf + r;
-                        const float v = (float)xf[q][s][e] * grow[r];
-                        const __bf16 v0 = (__bf16)v;
-                        const float r1 = v - (float)v0;
-                        const __bf16 v1 = (__bf16)r1;
-                        xw[q][0][e] = v0;
-                        xw[q][1][e] = v1;
-                        xw[q][2][e] = (__bf16)(r1 - (float)v1);
-                    }
+                    for (int r = 0; r < 4; r += 2) split3(xf[q][s], 4 * hf + r, grow[r], grow[r + 1], xw[q]);
                 }
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
@@ -601,14 +656,25 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, const Pl
     const size_t step = (size_t)p.slabs * K * SLAB;
     float* at = p.ends + ((size_t)w.slot0 * p.slabs + slab) * (size_t)(K * SLAB) + part * 1024 + threadIdx.x * 4;
     f32x4 H = *reinterpret_cast<const f32x4*>(at);
-#pragma unroll 4
-    for (int s = 1; s < w.count - 1; ++s) {
-        at += step;
-        const float d = p.decay[(w.slot0 + s) * p.slabs + slab];
-        const f32x4 L = *reinterpret_cast<const f32x4*>(at);
+    // loads of eight slots at a time are in flight before the first is stored over
+    for (int s = 1; s < w.count - 1; s += 8) {
+        const int m = min(8, w.count - 1 - s);
+        f32x4 L[8];
+        float d[8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) H[r] = fmaf(d, H[r], L[r]);
-        *reinterpret_cast<f32x4*>(at) = H;
+        for (int i = 0; i < 8; ++i) {
+            const int k = i < m ? i : 0;
+            L[i] = *reinterpret_cast<const f32x4*>(at + (k + 1) * step);
+            d[i] = p.decay[(w.slot0 + s + k) * p.slabs + slab];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= m) break;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) H[r] = fmaf(d[i], H[r], L[i][r]);
+            *reinterpret_cast<f32x4*>(at + (i + 1) * step) = H;
+        }
+        at += 8 * step;
     }
 }
 
@@ -641,6 +707,7 @@ Plan plan_of(int B, int T, int H, int HV, int K, int V, int N, bool packed, int 
     p.tiles = packed ? (long long)T / p.seg + N : (long long)N * p.per;
     p.slots = packed ? (T > p.seg ? (long long)T / p.seg : 0) : (long long)N * (p.per - 1);
     p.ends = p.starts = p.decay = nullptr;
+    p.steps = nullptr;
     return p;
 }
 
@@ -655,18 +722,32 @@ template <int K, bool FIRST> void launch_pass(const SsmArgs& a, const Plan& p, u
         hipLaunchKernelGGL((ssm_scan_bf16_kernel<K, 1, FIRST>), dim3(blocks), dim3(256), 0, a.stream, a, p);
 }
 
+// [ends][starts][steps][decay]
+inline size_t steps_bytes(int B, int T, int HV) { return (size_t)3 * HV * B * T * sizeof(float); }
+
 template <int K> hipError_t launch_k(const SsmArgs& a) {
     Plan p = plan_of(a.B, a.T, a.H, a.HV, K, a.V, a.N, a.cu_seqlens != nullptr, a.dtype);
     const long long first = p.slots * p.units, second = p.tiles * p.units;
     const long long join = p.slots > 0 ? (a.cu_seqlens ? p.slots : (long long)a.N) * p.slabs * (K * SLAB / 1024) : 0;
-    if (first > 0x7fffffffLL || second > 0x7fffffffLL || join > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    const int per = (a.T + C - 1) / C, hblocks = (a.HV + STEP_HEADS - 1) / STEP_HEADS;
+    const long long chunks = (a.cu_seqlens ? (long long)a.T / C + a.N : (long long)a.N * per) * hblocks;
+    if (first > 0x7fffffffLL || second > 0x7fffffffLL || join > 0x7fffffffLL || chunks > 0x7fffffffLL)
+        return hipErrorInvalidConfiguration;
+    char* ws = static_cast<char*>(a.workspace);
+    p.ends = reinterpret_cast<float*>(ws);
+    if (a.final_state && a.final_state == a.initial_state) p.starts = reinterpret_cast<float*>(ws + slots_bytes(p, K));
+    float* steps = reinterpret_cast<float*>(ws + 2 * slots_bytes(p, K));
+    p.steps = steps;
+    p.decay = reinterpret_cast<float*>(ws + 2 * slots_bytes(p, K) + steps_bytes(a.B, a.T, a.HV));
+    hipError_t err;
+    if (chunks > 0) {
+        hipLaunchKernelGGL(ssm_steps_kernel, dim3((unsigned)chunks), dim3(256), 0, a.stream, a, steps, per, hblocks);
+        err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
     if (p.slots > 0) {
-        char* ws = static_cast<char*>(a.workspace);
-        p.ends = reinterpret_cast<float*>(ws);
-        if (a.final_state && a.final_state == a.initial_state) p.starts = reinterpret_cast<float*>(ws + slots_bytes(p, K));
-        p.decay = reinterpret_cast<float*>(ws + 2 * slots_bytes(p, K));
         launch_pass<K, true>(a, p, (unsigned)first);
-        hipError_t err = hipGetLastError();
+        err = hipGetLastError();
         if (err != hipSuccess) return err;
         hipLaunchKernelGGL((ssm_join_kernel<K>), dim3((unsigned)join), dim3(256), 0, a.stream, a, p);
         err = hipGetLastError();
@@ -680,7 +761,7 @@ template <int K> hipError_t launch_k(const SsmArgs& a) {
 
 size_t ssm_chunk_workspace(int B, int T, int H, int HV, int K, int V, int N, bool packed, int dtype) {
     const Plan p = plan_of(B, T, H, HV, K, V, N, packed, dtype);
-    return 2 * slots_bytes(p, K) + (size_t)p.slots * p.slabs * sizeof(float);
+    return 2 * slots_bytes(p, K) + steps_bytes(B, T, HV) + (size_t)p.slots * p.slabs * sizeof(float);
 }
 
 hipError_t launch_ssm_chunk(const SsmArgs& a) { return a.K == 128 ? launch_k<128>(a) : launch_k<64>(a); }
