@@ -53,6 +53,15 @@ struct Work {
     long long slot0;      // its first slot
 };
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ long long uniform(long long v) {
+    return (long long)((unsigned long long)(unsigned)uniform((int)(v >> 32)) << 32 | (unsigned)uniform((int)v));
+}
+// the same for every lane, and known to be
+__device__ __forceinline__ Work uniform(const Work& w) {
+    return Work{uniform(w.n), uniform(w.s), uniform(w.count), uniform(w.len), uniform(w.row0), uniform(w.slot0)};
+}
+
 __device__ __forceinline__ Work second_pass_work(long long tile, const SsmArgs& a, const Plan& p) {
     const SeqTile s = seq_tile(tile, a.cu_seqlens, a.N, a.T, p.seg, p.per);
     Work w;
@@ -176,10 +185,11 @@ __device__ __forceinline__ double place_steps(const Step& v, int cl, Steps* s) {
 }
 
 // The state a segment starts from, in accumulators, and where one goes: [K][V] with this
-// lane's column `col`, or a slot in the accumulators' order.
+// lane's column `col` of the slab, or a slot in the accumulators' order (tile t of part
+// `part` of the slab's SLAB / 16 parts).
 template <int KT> __device__ __forceinline__ void load_start(f32x4 (&S)[KT], const SsmArgs& a, const Plan& p,
-                                                             const Work& w, int slab, bool first_pass) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
+                                                             const Work& w, int slab, int col, int part, bool first_pass) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
     const size_t per_slab = (size_t)KT * 16 * SLAB;
     const float* kept = nullptr;
     if (w.s > 0) {
@@ -188,7 +198,7 @@ template <int KT> __device__ __forceinline__ void load_start(f32x4 (&S)[KT], con
         kept = p.starts + ((size_t)w.slot0 * p.slabs + slab) * per_slab;
     } else if (a.initial_state) {
         const int vs = a.V / SLAB, hv = slab / vs;
-        const float* h0 = a.initial_state + ((size_t)w.n * a.HV + hv) * (size_t)(KT * 16) * a.V + (slab % vs) * SLAB + 16 * wave + l16;
+        const float* h0 = a.initial_state + ((size_t)w.n * a.HV + hv) * (size_t)(KT * 16) * a.V + (slab % vs) * SLAB + col;
 #pragma unroll
         for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -197,22 +207,21 @@ template <int KT> __device__ __forceinline__ void load_start(f32x4 (&S)[KT], con
     }
 #pragma unroll
     for (int t = 0; t < KT; ++t)
-        S[t] = kept ? *reinterpret_cast<const f32x4*>(kept + ((t * 4 + wave) * 64 + lane) * 4) : f32x4{0.f, 0.f, 0.f, 0.f};
+        S[t] = kept ? *reinterpret_cast<const f32x4*>(kept + ((t * 4 + part) * 64 + lane) * 4) : f32x4{0.f, 0.f, 0.f, 0.f};
 }
 template <int KT> __device__ __forceinline__ void store_slot(const f32x4 (&S)[KT], float* base, const Plan& p, long long slot,
-                                                             int slab) {
-    float* at = base + ((size_t)slot * p.slabs + slab) * (size_t)(KT * 16 * SLAB) + threadIdx.x * 4;
+                                                             int slab, int part) {
+    float* at = base + ((size_t)slot * p.slabs + slab) * (size_t)(KT * 16 * SLAB) + (part * 64 + (threadIdx.x & 63)) * 4;
 #pragma unroll
     for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4*>(at + t * 1024) = S[t];
 }
-template <int KT> __device__ __forceinline__ void store_final(const f32x4 (&S)[KT], const SsmArgs& a, int n, int slab) {
-    int tid = threadIdx.x;
+template <int KT> __device__ __forceinline__ void store_final(const f32x4 (&S)[KT], const SsmArgs& a, int n, int slab, int col) {
+    int g = (threadIdx.x & 63) >> 4;
     // the addresses are those load_start forms: keep the compiler from holding them in
     // registers (64 of them) all through the walk
-    asm volatile("" : "+v"(tid));
-    const int lane = tid & 63, wave = tid >> 6, l16 = lane & 15, g = lane >> 4;
+    asm volatile("" : "+v"(g));
     const int vs = a.V / SLAB, hv = slab / vs;
-    float* hT = a.final_state + ((size_t)n * a.HV + hv) * (size_t)(KT * 16) * a.V + (slab % vs) * SLAB + 16 * wave + l16;
+    float* hT = a.final_state + ((size_t)n * a.HV + hv) * (size_t)(KT * 16) * a.V + (slab % vs) * SLAB + col;
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -238,8 +247,8 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
     if (w.len < 0) return;
     const int vs = a.V / SLAB, hv = slab / vs, h = hv / (a.HV / a.H);
     f32x4 S[KT];
-    load_start(S, a, p, w, slab, FIRST);
-    if (FIRST && w.s == 0 && p.starts) store_slot(S, p.starts, p, w.slot0, slab);
+    load_start(S, a, p, w, slab, 16 * wave + l16, wave, FIRST);
+    if (FIRST && w.s == 0 && p.starts) store_slot(S, p.starts, p, w.slot0, slab, wave);
     const float skip = a.D ? a.D[hv] : 0.f;
     double total = 0.0;
 
@@ -346,22 +355,26 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
         }
     }
     if (FIRST) {
-        store_slot(S, p.ends, p, w.slot0 + w.s, slab);
+        store_slot(S, p.ends, p, w.slot0 + w.s, slab, wave);
         if (threadIdx.x == 0) p.decay[(w.slot0 + w.s) * p.slabs + slab] = exp2_fast((float)fmax(total, -1000.0));
     } else if (a.final_state && w.s == w.count - 1) {
-        store_final(S, a, w.n, slab);
+        store_final(S, a, w.n, slab, 16 * wave + l16);
     }
 }
 
 // ---------------------------------------------------------------------------------
-// bf16 inputs: the bf16 matrix cores, NS slabs of one b / c group a block.
+// bf16 inputs: the bf16 matrix cores, NS slabs of one b / c group a block. Two slabs: a wave
+// holds 32 columns of one of them (two column tiles), so that what it reads of b and c, the
+// most of its LDS traffic, serves twice; one slab: 16 columns.
 //   * c_i . b_j is exact bf16 products summed in fp32; M is rounded to bf16 once after its
 //     weights, and the state once as the operand of S^T c: half a bf16 step of every term,
 //     which is what y's own storage costs.
-//   * the state is kept to fp32: each weighted x is split into three bf16 (24 bits), so its
+//   * the state is kept to fp32: each weighted x is cut into three bf16 (24 bits), so its
 //     update is three products.
 //   * operands whose contraction runs over tokens (x and b down a column) are read from LDS
 //     transposed (ds_read_b64_tr_b16: four consecutive rows of a column a lane).
+//   * rows past the sequence's end are loaded as zeros and their stores dropped by the bounds
+//     of the buffer descriptors (made for every chunk), without branches.
 // Rows in LDS are 32 bytes longer than their data, and every eight rows begin 16 bytes
 // later: the transposed reads' half waves (8 rows x 32 bytes) and the row-wise 8-byte operand
 // reads' (16 rows x 16 bytes) then both meet every bank once.
@@ -370,17 +383,18 @@ constexpr int GAP = 16;   // elements
 template <int LD> __device__ __forceinline__ constexpr int row_at(int r) { return r * LD + 8 * (r >> 3); }
 
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
-// four consecutive rows (tokens 16 J + 4 g ..) of column c0 + l % 16 of a [C][LD] tile
-template <int LD> __device__ __forceinline__ bf16x4 read_col4(const __bf16* t, int J, int c0) {
-    const int lane = threadIdx.x & 63;
-    const __bf16* at = t + (row_at<LD>(lane >> 2) + 4 * (lane & 3)) + (row_at<LD>(16 * J) + c0);
-    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(at)));
+// four consecutive rows (tokens 16 J + 4 g ..) of one column: `t` points at this lane's part
+// of the tile, row (lane / 4) of 16 and the four columns lane % 4 stands for
+template <int LD> __device__ __forceinline__ bf16x4 read_col4(const __bf16* t, int J) {
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(t + row_at<LD>(16 * J))));
 }
 __device__ __forceinline__ bf16x8 join(bf16x4 u, bf16x4 v) { return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7); }
 // a row's 32 elements of step s, in accumulator order: 4 g .. +3 of both halves
-__device__ __forceinline__ bf16x8 read_row(const __bf16* row, int s, int g) {
-    return join(*reinterpret_cast<const bf16x4*>(row + 32 * s + 4 * g), *reinterpret_cast<const bf16x4*>(row + 32 * s + 16 + 4 * g));
+__device__ __forceinline__ bf16x8 read_row(const __bf16* row, int s) {
+    return join(*reinterpret_cast<const bf16x4*>(row + 32 * s), *reinterpret_cast<const bf16x4*>(row + 32 * s + 16));
 }
 // elements e and e + 1 of x times their weights, each cut into three bf16 whose sum is the
 // fp32 product exactly (8 + 8 + 8 bits, by truncation)
@@ -403,101 +417,115 @@ __device__ __forceinline__ f32x4 mma32(bf16x8 a, bf16x8 b, f32x4 c) { return Mma
 // where M's operand fragment of token block I, step s (token blocks 2s and 2s+1) is kept
 __device__ __forceinline__ constexpr int m_frag(int I, int s) { return I < 2 ? I : 2 * I - 2 + s; }
 
+// a descriptor of `bytes` bytes at p: loads past them give 0, stores there are dropped
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, unsigned bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+__device__ __forceinline__ bf16x8 buffer_piece(__amdgpu_buffer_rsrc_t r, unsigned at) {
+    return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+}
+
 template <int K, int NS, bool FIRST>
 __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, const Plan p) {
     constexpr int KT = K / 16, KS = K / 32;
+    constexpr int CT = NS;                                          // column tiles of a wave
     constexpr int LDK = K + GAP, LDX = SLAB + GAP;
     constexpr int NB = C * K / 8 / 256, NX = C * SLAB / 8 / 256;   // 16-byte pieces a thread
     constexpr int RB = 256 / (K / 8), RX = 256 / (SLAB / 8);       // rows between them
     __shared__ __attribute__((aligned(16))) __bf16 Bs[row_at<LDK>(C)], Cs[FIRST ? 8 : row_at<LDK>(C)], Xs[NS][row_at<LDX>(C)];
     __shared__ __attribute__((aligned(16))) __bf16 Ms[FIRST ? 1 : NS][FIRST ? 8 : 6 * 64 * 8];
     __shared__ Steps steps[2][NS];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int l16 = lane & 15, g = lane >> 4;
     const int slab0 = (int)(blockIdx.x % p.units) * NS;
     const long long tile = blockIdx.x / p.units;
-    const Work w = FIRST ? first_pass_work(tile, a, p) : second_pass_work(tile, a, p);
+    const Work w = uniform(FIRST ? first_pass_work(tile, a, p) : second_pass_work(tile, a, p));
     if (w.len < 0) return;
     const int vs = a.V / SLAB, h = slab0 / vs / (a.HV / a.H);
     const int begin = w.s * p.seg;
     const int stop = w.len - begin < p.seg ? w.len : begin + p.seg;
+    // this wave's columns: tile u's column m (an accumulator's lane % 16, its operand's row)
+    // is base + 8 (m / 4) + 4 u + m % 4 of its slab, so that a lane's four rows of two tiles
+    // are 16 contiguous bytes of y; with one tile simply base + m
+    const int q = NS == 2 ? wave >> 1 : 0;
+    const int base = NS == 2 ? 32 * (wave & 1) : 16 * wave;
+    const int slab = slab0 + q;
+    auto column = [&](int u) { return NS == 2 ? base + 8 * (l16 >> 2) + 4 * u + (l16 & 3) : base + l16; };
+    auto part = [&](int u) { return NS == 2 ? 2 * (wave & 1) + u : wave; };
 
-    // this thread's pieces of a chunk, as 32-bit offsets from the chunk's row (a stride is at
-    // most 2^24); past the sequence's end the last row stands in (its weights are 0 there)
+    // this thread's pieces of a chunk, as byte offsets from the chunk's row (a stride is
+    // under 2^24), and where they go in LDS (rows 16 i, RB i and RX i are whole groups of
+    // eight, so their offsets there add)
     const int tb = tid / (K / 8), tx = tid / (SLAB / 8);
+    const unsigned kb = tid % (K / 8) * 8, kx = tid % (SLAB / 8) * 8;
     const __bf16* bp = static_cast<const __bf16*>(a.b) + w.row0 * a.b_stride + (size_t)h * K;
     const __bf16* cp = static_cast<const __bf16*>(a.c) + w.row0 * a.c_stride + (size_t)h * K;
     const __bf16* xp = static_cast<const __bf16*>(a.x) + w.row0 * a.x_stride + (size_t)slab0 * SLAB;
-    const unsigned kb = tid % (K / 8) * 8, kx = tid % (SLAB / 8) * 8;
-    // where they go in LDS, and this lane's place in a row-wise operand (rows 16 i, RB i and
-    // RX i are whole groups of eight, so their offsets add)
+    const unsigned bs2 = (unsigned)a.b_stride * 2, cs2 = (unsigned)a.c_stride * 2, xs2 = (unsigned)a.x_stride * 2;
+    const unsigned b_at = tb * bs2 + kb * 2, c_at = tb * cs2 + kb * 2, x_at = tx * xs2 + kx * 2;
     const int putk = row_at<LDK>(tb) + kb, putx = row_at<LDX>(tx) + kx;
-    const int rowk = row_at<LDK>(l16) + 4 * g, rowx = row_at<LDX>(l16) + 16 * wave + 4 * g;
+    // this lane's place in a row-wise operand, in a transposed one of b, and of x
+    const int rowk = row_at<LDK>(l16) + 4 * g;
+    const int colb = row_at<LDK>(lane >> 2) + 4 * (lane & 3);
+    const int colx = row_at<LDX>(lane >> 2) + base + (NS == 2 ? 8 : 4) * (lane & 3);
     bf16x8 rb[NB], rc[FIRST ? 1 : NB], rx[NS][NX];
-    auto piece = [](const __bf16* base, unsigned bytes) {
-        return *reinterpret_cast<const bf16x8*>(reinterpret_cast<const char*>(base) + bytes);
-    };
     auto fetch = [&](int p0) {
         const unsigned last = min(w.len - p0, C) - 1;
-        const __bf16* bc = bp + p0 * a.b_stride;
-        const __bf16* cc = cp + p0 * a.c_stride;
-        const __bf16* xc = xp + p0 * a.x_stride;
+        const auto bd = buffer_of(bp + p0 * a.b_stride, last * bs2 + K * 2);
+        const auto cd = buffer_of(cp + p0 * a.c_stride, last * cs2 + K * 2);
+        const auto xd = buffer_of(xp + p0 * a.x_stride, last * xs2 + NS * SLAB * 2);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const unsigned t = min((unsigned)(tb + i * RB), last);
-            rb[i] = piece(bc, (__umul24(t, (unsigned)a.b_stride) + kb) * 2);
-            if constexpr (!FIRST) rc[i] = piece(cc, (__umul24(t, (unsigned)a.c_stride) + kb) * 2);
+            rb[i] = buffer_piece(bd, b_at + i * RB * bs2);
+            if constexpr (!FIRST) rc[i] = buffer_piece(cd, c_at + i * RB * cs2);
         }
 #pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const unsigned at = __umul24(min((unsigned)(tx + i * RX), last), (unsigned)a.x_stride) + kx;
+        for (int i = 0; i < NX; ++i)
 #pragma unroll
-            for (int q = 0; q < NS; ++q) rx[q][i] = piece(xc + q * SLAB, at * 2);
-        }
+            for (int v = 0; v < NS; ++v) rx[v][i] = buffer_piece(xd, x_at + i * RX * xs2 + v * SLAB * 2);
     };
-    // wave q < NS places slab q's steps, a chunk ahead, from what it loads two chunks ahead
-    const int my_hv = (slab0 + (wave < NS ? wave : 0)) / vs;
+    // wave 3 - v (the ones with the fewest of M's tiles) places slab v's steps, a chunk ahead,
+    // from what it loads two chunks ahead
+    const int mine = 3 - wave;
+    const int my_hv = (slab0 + (mine < NS ? mine : 0)) / vs;
     Step ahead{0.f, 0.f, 0.f};
     double total = 0.0;
     auto fetch_steps = [&](int p0) {
-        if (wave < NS) ahead = load_step(a, p, w.row0 + p0, min(w.len - p0, C), my_hv);
+        if (mine < NS) ahead = load_step(a, p, w.row0 + p0, min(w.len - p0, C), my_hv);
     };
     auto form_steps = [&](int p0) {
-        if (wave < NS) total += place_steps(ahead, min(w.len - p0, C), &steps[(p0 / C) & 1][wave]);
+        if (mine < NS) total += place_steps(ahead, min(w.len - p0, C), &steps[(p0 / C) & 1][mine]);
     };
     if (begin < stop) {
         fetch_steps(begin);
         fetch(begin);
     }
 
-    f32x4 S[NS][KT];
+    f32x4 S[CT][KT];
 #pragma unroll
-    for (int q = 0; q < NS; ++q) load_start(S[q], a, p, w, slab0 + q, FIRST);
+    for (int u = 0; u < CT; ++u) load_start(S[u], a, p, w, slab, column(u), part(u), FIRST);
     if (FIRST && w.s == 0 && p.starts)
 #pragma unroll
-        for (int q = 0; q < NS; ++q) store_slot(S[q], p.starts, p, w.slot0, slab0 + q);
-    float skip[NS];
-#pragma unroll
-    for (int q = 0; q < NS; ++q) skip[q] = a.D ? a.D[(slab0 + q) / vs] : 0.f;
+        for (int u = 0; u < CT; ++u) store_slot(S[u], p.starts, p, w.slot0, slab, part(u));
+    const float skip = a.D ? a.D[slab / vs] : 0.f;
     if constexpr (!FIRST) {
         // the halves of M's fragments above the diagonal: token blocks 1 of I = 0, 3 of I = 2
         if (wave == 0)
 #pragma unroll
-            for (int q = 0; q < NS; ++q) {
-                *reinterpret_cast<bf16x4*>(Ms[q] + (m_frag(0, 0) * 64 + lane) * 8 + 4) = bf16x4{};
-                *reinterpret_cast<bf16x4*>(Ms[q] + (m_frag(2, 1) * 64 + lane) * 8 + 4) = bf16x4{};
+            for (int v = 0; v < NS; ++v) {
+                *reinterpret_cast<bf16x4*>(Ms[v] + (m_frag(0, 0) * 64 + lane) * 8 + 4) = bf16x4{};
+                *reinterpret_cast<bf16x4*>(Ms[v] + (m_frag(2, 1) * 64 + lane) * 8 + 4) = bf16x4{};
             }
     }
     if (begin < stop) {
         form_steps(begin);
         if (begin + C < stop) fetch_steps(begin + C);
     }
-    const unsigned y_row = p.slabs * SLAB;
-    const unsigned y_at = l16 * y_row + 16 * wave + 4 * g;
-    __bf16* yp = static_cast<__bf16*>(a.y) + (w.row0 + begin) * (long long)y_row + slab0 * SLAB;
+    const unsigned y_row = p.slabs * SLAB * 2;
+    const unsigned y_at = l16 * y_row + (base + 4 * NS * g) * 2;
+    const __bf16* yp = static_cast<const __bf16*>(a.y) + (w.row0 + begin) * (long long)(p.slabs * SLAB) + slab * SLAB;
 
-    for (int p0 = begin; p0 < stop; p0 += C, yp += C * (long long)y_row) {
-        const int cl = w.len - p0 < C ? w.len - p0 : C;
+    for (int p0 = begin; p0 < stop; p0 += C, yp += C * (long long)(p.slabs * SLAB)) {
         const Steps* st = steps[(p0 / C) & 1];
         lds_barrier();   // the last chunk's readers are done
 #pragma unroll
@@ -508,138 +536,141 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
 #pragma unroll
         for (int i = 0; i < NX; ++i)
 #pragma unroll
-            for (int q = 0; q < NS; ++q) *reinterpret_cast<bf16x8*>(Xs[q] + putx + row_at<LDX>(i * RX)) = rx[q][i];
+            for (int v = 0; v < NS; ++v) *reinterpret_cast<bf16x8*>(Xs[v] + putx + row_at<LDX>(i * RX)) = rx[v][i];
         lds_barrier();
         if (p0 + C < stop) {   // in flight while this chunk is worked on
             fetch(p0 + C);
             form_steps(p0 + C);
             if (p0 + 2 * C < stop) fetch_steps(p0 + 2 * C);
         }
-
+        // this wave's columns of x down the tokens
+        bf16x8 xf[CT][2];
+#pragma unroll
+        for (int u = 0; u < CT; ++u)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                xf[u][s] = join(read_col4<LDX>(Xs[q] + colx + 4 * u, 2 * s), read_col4<LDX>(Xs[q] + colx + 4 * u, 2 * s + 1));
+        f32x4 acc[FIRST ? 1 : CT][FIRST ? 1 : 4];
         if constexpr (!FIRST) {
-            // M^T: wave w forms token rows J <= w of token columns 16 w ..
-            bf16x8 cf[KS];
-            const int i = 16 * wave + l16;
+            // M^T's ten tiles (token rows J, columns I >= J), three or two a wave: 4 bits of
+            // I and J each, the first tile lowest
+            const unsigned tiles = wave == 0 ? 0x323130u : wave == 1 ? 0x212033u : wave == 2 ? 0x1022u : 0x0011u;
+            const int count = wave < 2 ? 3 : 2;
+            for (int n = 0; n < count; ++n) {
+                const int I = tiles >> (8 * n + 4) & 15, J = tiles >> (8 * n) & 15;
+                const int i = 16 * I + l16, j0 = 16 * J + 4 * g;
+                f32x4 cb = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int s = 0; s < KS; ++s) cf[s] = read_row(Cs + rowk + row_at<LDK>(16) * wave, s, 0);
+                for (int s = 0; s < KS; ++s)
+                    cb = mma32(read_row(Bs + rowk + row_at<LDK>(16) * J, s), read_row(Cs + rowk + row_at<LDK>(16) * I, s), cb);
 #pragma unroll
-            for (int J = 0; J < 4; ++J) {
-                if (J > wave) break;
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < KS; ++s) acc = mma32(read_row(Bs + rowk + row_at<LDK>(16 * J), s, 0), cf[s], acc);
-                const int j0 = 16 * J + 4 * g;
-#pragma unroll
-                for (int q = 0; q < NS; ++q) {
-                    const f32x4 hj = *reinterpret_cast<const f32x4*>(st[q].hi + j0), lj = *reinterpret_cast<const f32x4*>(st[q].lo + j0);
-                    const f32x4 dj = *reinterpret_cast<const f32x4*>(st[q].dt + j0);
-                    const float hi = st[q].hi[i], lo = st[q].lo[i];
+                for (int v = 0; v < NS; ++v) {
+                    const f32x4 hj = *reinterpret_cast<const f32x4*>(st[v].hi + j0), lj = *reinterpret_cast<const f32x4*>(st[v].lo + j0);
+                    const f32x4 dj = *reinterpret_cast<const f32x4*>(st[v].dt + j0);
+                    const float hi = st[v].hi[i], lo = st[v].lo[i];
                     bf16x4 m;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float e = exp2_fast((hi - hj[r]) + (lo - lj[r])) * dj[r];
-                        m[r] = (__bf16)(J < wave || j0 + r <= i ? acc[r] * e : 0.f);
+                        m[r] = (__bf16)(j0 + r <= i ? cb[r] * e : 0.f);
                     }
-                    *reinterpret_cast<bf16x4*>(Ms[q] + (m_frag(wave, J >> 1) * 64 + lane) * 8 + 4 * (J & 1)) = m;
+                    *reinterpret_cast<bf16x4*>(Ms[v] + (m_frag(I, J >> 1) * 64 + lane) * 8 + 4 * (J & 1)) = m;
                 }
             }
-        }
-        // this wave's columns of x down the tokens
-        bf16x8 xf[NS][2];
+            // S^T c of the chunk's four token blocks, scaled by the tokens' decays
+            bf16x8 sf[CT][KS];
 #pragma unroll
-        for (int q = 0; q < NS; ++q)
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                xf[q][s] = join(read_col4<LDX>(Xs[q], 2 * s, 16 * wave), read_col4<LDX>(Xs[q], 2 * s + 1, 16 * wave));
-        if constexpr (!FIRST) {
-            lds_barrier();
-            bf16x8 sf[NS][KS];
-#pragma unroll
-            for (int q = 0; q < NS; ++q)
+            for (int u = 0; u < CT; ++u)
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        sf[q][s][r] = (__bf16)S[q][2 * s][r];
-                        sf[q][s][4 + r] = (__bf16)S[q][2 * s + 1][r];
-                    }
-            // two blocks of tokens at a time, so that their chains of products interleave
-#pragma unroll
-            for (int I = 0; I < 4; I += 2) {
-                if (16 * I >= cl) break;
-                f32x4 acc[NS][2] = {};
-#pragma unroll
-                for (int s = 0; s < KS; ++s)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const bf16x8 cf = read_row(Cs + rowk + row_at<LDK>(16 * (I + k)), s, 0);
-#pragma unroll
-                        for (int q = 0; q < NS; ++q) acc[q][k] = mma32(sf[q][s], cf, acc[q][k]);
+                        sf[u][s][r] = (__bf16)S[u][2 * s][r];
+                        sf[u][s][4 + r] = (__bf16)S[u][2 * s + 1][r];
                     }
 #pragma unroll
-                for (int q = 0; q < NS; ++q) {
+            for (int I = 0; I < 4; ++I) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float f = st[q].fall[16 * (I + k) + l16];
+                for (int u = 0; u < CT; ++u) acc[u][I] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[q][k][r] *= f;
-                    }
+                for (int s = 0; s < KS; ++s) {
+                    const bf16x8 cf = read_row(Cs + rowk + row_at<LDK>(16 * I), s);
 #pragma unroll
-                    for (int s = 0; s <= (I >> 1); ++s)
+                    for (int u = 0; u < CT; ++u) acc[u][I] = mma32(sf[u][s], cf, acc[u][I]);
+                }
+            }
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            acc[q][k] = mma32(xf[q][s], *reinterpret_cast<const bf16x8*>(Ms[q] + (m_frag(I + k, s) * 64 + lane) * 8), acc[q][k]);
+            for (int I = 0; I < 4; ++I) {
+                const float f = st[q].fall[16 * I + l16];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        // columns 16 wave + 4 g .. +3 of token i
-                        const int i = 16 * (I + k) + l16;
-                        const bf16x4 xi = *reinterpret_cast<const bf16x4*>(Xs[q] + rowx + row_at<LDX>(16 * (I + k)));
-                        bf16x4 out;
+                for (int u = 0; u < CT; ++u)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) out[r] = (__bf16)fmaf(skip[q], (float)xi[r], acc[q][k][r]);
-                        if (i < cl) *reinterpret_cast<bf16x4*>(reinterpret_cast<char*>(yp + q * SLAB) + (y_at + 16 * (I + k) * y_row) * 2) = out;
-                    }
+                    for (int r = 0; r < 4; ++r) acc[u][I][r] *= f;
+            }
+            lds_barrier();   // M is there
+            const auto yd = buffer_of(yp, (min(w.len - p0, C) - 1) * y_row + SLAB * 2);
+#pragma unroll
+            for (int I = 0; I < 4; ++I) {
+#pragma unroll
+                for (int s = 0; s <= (I >> 1); ++s) {
+                    const bf16x8 m = *reinterpret_cast<const bf16x8*>(Ms[q] + (m_frag(I, s) * 64 + lane) * 8);
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) acc[u][I] = mma32(xf[u][s], m, acc[u][I]);
+                }
+                // columns base + 4 NS g .. of token 16 I + l % 16
+                const __bf16* xi = Xs[q] + row_at<LDX>(l16) + base + 4 * NS * g + row_at<LDX>(16 * I);
+                if constexpr (NS == 2) {
+                    const bf16x8 x8 = *reinterpret_cast<const bf16x8*>(xi);
+                    bf16x8 out;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) out[e] = (__bf16)fmaf(skip, (float)x8[e], acc[e >> 2][I][e & 3]);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, out), yd, y_at + I * 16 * y_row, 0, 0);
+                } else {
+                    const bf16x4 x4 = *reinterpret_cast<const bf16x4*>(xi);
+                    bf16x4 out;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) out[e] = (__bf16)fmaf(skip, (float)x4[e], acc[0][I][e]);
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, out), yd, y_at + I * 16 * y_row, 0, 0);
                 }
             }
         }
         // the state at the chunk's end
+        const float all = st[q].all;
 #pragma unroll
-        for (int q = 0; q < NS; ++q) {
-            const float all = st[q].all;
+        for (int u = 0; u < CT; ++u)
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[q][t][r] *= all;
-        }
+                for (int r = 0; r < 4; ++r) S[u][t][r] *= all;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            bf16x8 xw[NS][3];
+            bf16x8 xw[CT][3];
 #pragma unroll
-            for (int q = 0; q < NS; ++q)
+            for (int hf = 0; hf < 2; ++hf) {
+                const f32x4 grow = *reinterpret_cast<const f32x4*>(st[q].grow + 32 * s + 16 * hf + 4 * g);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const f32x4 grow = *reinterpret_cast<const f32x4*>(st[q].grow + 32 * s + 16 * hf + 4 * g);
+                for (int u = 0; u < CT; ++u)
 #pragma unroll
-                    for (int r = 0; r < 4; r += 2) split3(xf[q][s], 4 * hf + r, grow[r], grow[r + 1], xw[q]);
-                }
+                    for (int r = 0; r < 4; r += 2) split3(xf[u][s], 4 * hf + r, grow[r], grow[r + 1], xw[u]);
+            }
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
-                const bf16x8 bt = join(read_col4<LDK>(Bs, 2 * s, 16 * t), read_col4<LDK>(Bs, 2 * s + 1, 16 * t));
+                const bf16x8 bt = join(read_col4<LDK>(Bs + colb + 16 * t, 2 * s), read_col4<LDK>(Bs + colb + 16 * t, 2 * s + 1));
 #pragma unroll
-                for (int q = 0; q < NS; ++q)
+                for (int k = 2; k >= 0; --k)
 #pragma unroll
-                    for (int u = 2; u >= 0; --u) S[q][t] = mma32(bt, xw[q][u], S[q][t]);
+                    for (int u = 0; u < CT; ++u) S[u][t] = mma32(bt, xw[u][k], S[u][t]);
             }
         }
     }
     if constexpr (FIRST) {
 #pragma unroll
-        for (int q = 0; q < NS; ++q) store_slot(S[q], p.ends, p, w.slot0 + w.s, slab0 + q);
-        if (wave < NS && lane == 0)
-            p.decay[(w.slot0 + w.s) * p.slabs + slab0 + wave] = exp2_fast((float)fmax(total, -1000.0));
+        for (int u = 0; u < CT; ++u) store_slot(S[u], p.ends, p, w.slot0 + w.s, slab, part(u));
+        if (mine < NS && lane == 0)
+            p.decay[(w.slot0 + w.s) * p.slabs + slab0 + mine] = exp2_fast((float)fmax(total, -1000.0));
     } else if (a.final_state && w.s == w.count - 1) {
 #pragma unroll
-        for (int q = 0; q < NS; ++q) store_final(S[q], a, w.n, slab0 + q);
+        for (int u = 0; u < CT; ++u) store_final(S[u], a, w.n, slab, column(u));
     }
 }
 
