@@ -44,6 +44,8 @@ struct Plan {
                           // is initial_state and would be overwritten before it is read
     float* decay;         // [slots][slabs]
     const float* steps;   // [3][HV][rows], see ssm_steps_kernel
+    const int* order;     // the second pass's segments, longest first, or NULL
+    int* cuts;            // packed: whether any sequence is longer than a segment, or NULL
 };
 
 struct Work {
@@ -62,8 +64,22 @@ __device__ __forceinline__ Work uniform(const Work& w) {
     return Work{uniform(w.n), uniform(w.s), uniform(w.count), uniform(w.len), uniform(w.row0), uniform(w.slot0)};
 }
 
+// A block's segment and unit. Blocks go to the chip's eight dies in turn, each with its own
+// L2: the units of a segment, which read the same b and c, are kept on one.
+__device__ __forceinline__ void place_of(long long block, long long tiles, int units, long long* tile, int* unit) {
+    const long long whole = tiles / 8 * 8;
+    if (block < whole * units) {
+        const long long j = block / 8;
+        *tile = j / units * 8 + block % 8;
+        *unit = (int)(j % units);
+    } else {
+        *tile = block / units;
+        *unit = (int)(block % units);
+    }
+}
+
 __device__ __forceinline__ Work second_pass_work(long long tile, const SsmArgs& a, const Plan& p) {
-    const SeqTile s = seq_tile(tile, a.cu_seqlens, a.N, a.T, p.seg, p.per);
+    const SeqTile s = seq_tile(p.order ? p.order[tile] : tile, a.cu_seqlens, a.N, a.T, p.seg, p.per);
     Work w;
     w.n = s.n;
     w.len = s.len;
@@ -82,6 +98,7 @@ __device__ __forceinline__ Work first_pass_work(long long slot, const SsmArgs& a
     w.s = 0;
     w.count = 0;
     w.row0 = w.slot0 = 0;
+    if (p.cuts && !*p.cuts) return w;
     if (!a.cu_seqlens) {
         w.n = (int)(slot / (p.per - 1));
         w.s = (int)(slot % (p.per - 1));
@@ -120,39 +137,109 @@ struct alignas(16) Steps {
 
 // dt' and the running sums of the log2 decay inside each chunk, for every row and head:
 // steps[0], [1], [2] are dt', hi and lo as [HV][rows] (the sums are formed in fp64, since
-// the exponents are differences of them, and kept as hi + lo). One block: a chunk of a
+// the exponents are differences of them) and kept as hi + lo. One block: a chunk of a
 // sequence and 8 heads; a wave takes a head, its lane a token. Formed once instead of in
 // every block that walks the chunk, where one wave's transcendentals and 64-bit prefix sums
-// held up the others (first pass of 32768 x 64 heads: 157 us with, 112 without them).
+// held up the others (first pass of 32768 tokens x 64 heads: 157 us with, 129 without them).
 constexpr int STEP_HEADS = 8;
-__global__ __launch_bounds__(256) void ssm_steps_kernel(const SsmArgs a, float* steps, int per, int hblocks) {
+
+// inclusive prefix sum over the wave: within the four rows of 16 lanes by lane shifts, then
+// the sums of the rows before (no LDS)
+template <int N> __device__ __forceinline__ double row_shr(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, 0x110 + N, 0xf, 0xf, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), 0x110 + N, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_value(double v, int l) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), l) << 32 |
+                                          (uint32_t)__builtin_amdgcn_readlane((int)b, l));
+}
+__device__ __forceinline__ double wave_scan(double v) {
+    v += row_shr<1>(v);
+    v += row_shr<2>(v);
+    v += row_shr<4>(v);
+    v += row_shr<8>(v);
+    const double a = lane_value(v, 15), b = a + lane_value(v, 31), c = b + lane_value(v, 47);
+    const int row = (threadIdx.x & 63) >> 4;
+    return v + (row == 0 ? 0.0 : row == 1 ? a : row == 2 ? b : c);
+}
+
+// The second pass's segments by length, longest first (their order changes no result): a
+// packed batch of ragged prompts then ends with short ones. 64 slots of 1..1024 tokens x 16
+// heads on 512 resident blocks: 16 chunks for the busiest instead of 24. One block; a
+// counting sort over 256 lengths.
+constexpr int ORDER_MAX = 4096;
+__device__ void order_segments(const SsmArgs& a, const Plan& p, int* order) {
+    __shared__ uint8_t bin[ORDER_MAX];
+    __shared__ int count[256];
+    const int tid = threadIdx.x;
+    count[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < (int)p.tiles; i += 256) {
+        const SeqTile s = seq_tile(i, a.cu_seqlens, a.N, a.T, p.seg, p.per);
+        const int len = max(min(s.len - s.pos, p.seg), 0);
+        bin[i] = (uint8_t)((long long)((len + C - 1) / C) * 255 / (p.seg / C));
+        atomicAdd(&count[bin[i]], 1);
+    }
+    __syncthreads();
+    // places of a length: after all longer ones (sums from the longest down, thread tid
+    // holding length 255 - tid)
+    __shared__ int wave_sum[4];
+    const int mine = count[255 - tid];
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+        const int v = __shfl_up(upto, o, 64);
+        if ((tid & 63) >= o) upto += v;
+    }
+    if ((tid & 63) == 63) wave_sum[tid >> 6] = upto;
+    __syncthreads();
+    for (int k = 0; k < tid >> 6; ++k) upto += wave_sum[k];
+    count[255 - tid] = upto - mine;
+    __syncthreads();
+    for (int i = tid; i < (int)p.tiles; i += 256) order[atomicAdd(&count[bin[i]], 1)] = i;
+}
+
+__global__ __launch_bounds__(256) void ssm_steps_kernel(const SsmArgs a, const Plan p, float* steps, int* order, int per, int hblocks) {
     __shared__ float raw[C][STEP_HEADS + 1];
-    if (blockIdx.x == 0) flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
+    __shared__ double rate[STEP_HEADS];
+    if (blockIdx.x == gridDim.x - 1) {   // the block behind the chunks'
+        flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
+        if (p.cuts && threadIdx.x < 64) {   // does a sequence of this batch have to be cut at all
+            int most = 0;
+            for (int n = threadIdx.x; n < a.N; n += 64) most = max(most, a.cu_seqlens[n + 1] - a.cu_seqlens[n]);
+#pragma unroll
+            for (int o = 32; o > 0; o /= 2) most = max(most, __shfl_xor(most, o, 64));
+            if (threadIdx.x == 0) *p.cuts = most > p.seg;
+        }
+        if (order) order_segments(a, p, order);
+        return;
+    }
     const int h0 = (int)(blockIdx.x % hblocks) * STEP_HEADS;
     const SeqTile s = seq_tile(blockIdx.x / hblocks, a.cu_seqlens, a.N, a.T, C, per);
     const int cl = min(s.len - s.pos, C);
     if (cl <= 0) return;
     const long long row = s.row0 + s.pos, rows = (long long)a.B * a.T;
+    if (threadIdx.x < STEP_HEADS && h0 + threadIdx.x < a.HV) rate[threadIdx.x] = ssm_rate(a.A_log[h0 + threadIdx.x]);
     for (int i = threadIdx.x; i < C * STEP_HEADS; i += 256) {
         const int t = i / STEP_HEADS, hv = i % STEP_HEADS;
         if (t < cl && h0 + hv < a.HV) raw[t][hv] = load_scalar(a.dt, a.dt_dtype, (row + t) * a.dt_stride + h0 + hv);
     }
     __syncthreads();
     const int j = threadIdx.x & 63;
-    for (int k = threadIdx.x >> 6; k < STEP_HEADS && h0 + k < a.HV; k += 4) {
-        const int hv = h0 + k;
+#pragma unroll
+    for (int n = 0; n < STEP_HEADS / 4; ++n) {
+        const int k = (threadIdx.x >> 6) + 4 * n, hv = min(h0 + k, a.HV - 1);
         float dt = 0.f;
         double cum = 0.0;
         if (j < cl) {
-            dt = ssm_step(raw[j][k], a.dt_bias ? a.dt_bias[hv] : 0.f, a.softplus);
-            cum = ssm_log2_decay(dt, a.A_log[hv]);
+            dt = ssm_step(raw[j][min(k, a.HV - 1 - h0)], a.dt_bias ? a.dt_bias[hv] : 0.f, a.softplus);
+            cum = ssm_log2_decay(dt, rate[hv - h0]);
         }
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-            const double up = __shfl_up(cum, o, 64);
-            if (j >= o) cum += up;
-        }
-        if (j < cl) {
+        cum = wave_scan(cum);
+        if (j < cl && h0 + k < a.HV) {
             const float hi = (float)cum;
             const long long at = (long long)hv * rows + row + j;
             steps[at] = dt;
@@ -241,8 +328,9 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
     __shared__ Steps st;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int l16 = lane & 15, g = lane >> 4;
-    const int slab = (int)(blockIdx.x % p.slabs);
-    const long long tile = blockIdx.x / p.slabs;
+    long long tile;
+    int slab;
+    place_of(blockIdx.x, FIRST ? p.slots : p.tiles, p.units, &tile, &slab);
     const Work w = FIRST ? first_pass_work(tile, a, p) : second_pass_work(tile, a, p);
     if (w.len < 0) return;
     const int vs = a.V / SLAB, hv = slab / vs, h = hv / (a.HV / a.H);
@@ -425,33 +513,37 @@ __device__ __forceinline__ bf16x8 buffer_piece(__amdgpu_buffer_rsrc_t r, unsigne
     return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
 }
 
-template <int K, int NS, bool FIRST>
-__global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, const Plan p) {
+template <int K, int NS, int WAVES, bool FIRST>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_kernel(const SsmArgs a, const Plan p) {
     constexpr int KT = K / 16, KS = K / 32;
-    constexpr int CT = NS;                                          // column tiles of a wave
+    constexpr int THREADS = 64 * WAVES;
+    constexpr int CT = 4 * NS / WAVES;                                          // column tiles of a wave
     constexpr int LDK = K + GAP, LDX = SLAB + GAP;
-    constexpr int NB = C * K / 8 / 256, NX = C * SLAB / 8 / 256;   // 16-byte pieces a thread
-    constexpr int RB = 256 / (K / 8), RX = 256 / (SLAB / 8);       // rows between them
+    constexpr int NB = C * K / 8 / THREADS, NX = C * SLAB / 8 / THREADS;   // 16-byte pieces a thread
+    constexpr int RB = THREADS / (K / 8), RX = THREADS / (SLAB / 8);       // rows between them
     __shared__ __attribute__((aligned(16))) __bf16 Bs[row_at<LDK>(C)], Cs[FIRST ? 8 : row_at<LDK>(C)], Xs[NS][row_at<LDX>(C)];
     __shared__ __attribute__((aligned(16))) __bf16 Ms[FIRST ? 1 : NS][FIRST ? 8 : 6 * 64 * 8];
     __shared__ Steps steps[2][NS];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int l16 = lane & 15, g = lane >> 4;
-    const int slab0 = (int)(blockIdx.x % p.units) * NS;
-    const long long tile = blockIdx.x / p.units;
+    long long tile;
+    int slab0;
+    place_of(blockIdx.x, FIRST ? p.slots : p.tiles, p.units, &tile, &slab0);
+    slab0 *= NS;
     const Work w = uniform(FIRST ? first_pass_work(tile, a, p) : second_pass_work(tile, a, p));
     if (w.len < 0) return;
     const int vs = a.V / SLAB, h = slab0 / vs / (a.HV / a.H);
     const int begin = w.s * p.seg;
     const int stop = w.len - begin < p.seg ? w.len : begin + p.seg;
-    // this wave's columns: tile u's column m (an accumulator's lane % 16, its operand's row)
-    // is base + 8 (m / 4) + 4 u + m % 4 of its slab, so that a lane's four rows of two tiles
-    // are 16 contiguous bytes of y; with one tile simply base + m
-    const int q = NS == 2 ? wave >> 1 : 0;
-    const int base = NS == 2 ? 32 * (wave & 1) : 16 * wave;
+    // this wave's columns. Two slabs a block: tile u of a half slab (32 columns from base on)
+    // has column base + 8 (m / 4) + 4 u + m % 4 at m (an accumulator's lane % 16, its operand's
+    // row), so that a lane's four rows of a half's two tiles are 16 contiguous bytes of y; a
+    // wave holds both (four waves) or one (eight). One slab: base + m.
+    const int q = CT == 2 ? wave >> 1 : wave >> 2;
+    const int base = CT == 2 ? 32 * (wave & 1) : NS == 2 ? 32 * (wave >> 1 & 1) + 4 * (wave & 1) : 16 * wave;
     const int slab = slab0 + q;
     auto column = [&](int u) { return NS == 2 ? base + 8 * (l16 >> 2) + 4 * u + (l16 & 3) : base + l16; };
-    auto part = [&](int u) { return NS == 2 ? 2 * (wave & 1) + u : wave; };
+    auto part = [&](int u) { return CT == 2 ? 2 * (wave & 1) + u : wave & 3; };
 
     // this thread's pieces of a chunk, as byte offsets from the chunk's row (a stride is
     // under 2^24), and where they go in LDS (rows 16 i, RB i and RX i are whole groups of
@@ -467,7 +559,7 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
     // this lane's place in a row-wise operand, in a transposed one of b, and of x
     const int rowk = row_at<LDK>(l16) + 4 * g;
     const int colb = row_at<LDK>(lane >> 2) + 4 * (lane & 3);
-    const int colx = row_at<LDX>(lane >> 2) + base + (NS == 2 ? 8 : 4) * (lane & 3);
+    const int colx = row_at<LDX>(lane >> 2) + base + 4 * NS * (lane & 3);
     bf16x8 rb[NB], rc[FIRST ? 1 : NB], rx[NS][NX];
     auto fetch = [&](int p0) {
         const unsigned last = min(w.len - p0, C) - 1;
@@ -486,7 +578,7 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
     };
     // wave 3 - v (the ones with the fewest of M's tiles) places slab v's steps, a chunk ahead,
     // from what it loads two chunks ahead
-    const int mine = 3 - wave;
+    const int mine = WAVES - 1 - wave;
     const int my_hv = (slab0 + (mine < NS ? mine : 0)) / vs;
     Step ahead{0.f, 0.f, 0.f};
     double total = 0.0;
@@ -522,7 +614,7 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
         if (begin + C < stop) fetch_steps(begin + C);
     }
     const unsigned y_row = p.slabs * SLAB * 2;
-    const unsigned y_at = l16 * y_row + (base + 4 * NS * g) * 2;
+    const unsigned y_at = l16 * y_row + (base + 4 * CT * g) * 2;
     const __bf16* yp = static_cast<const __bf16*>(a.y) + (w.row0 + begin) * (long long)(p.slabs * SLAB) + slab * SLAB;
 
     for (int p0 = begin; p0 < stop; p0 += C, yp += C * (long long)(p.slabs * SLAB)) {
@@ -554,6 +646,7 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
         if constexpr (!FIRST) {
             // M^T's ten tiles (token rows J, columns I >= J), three or two a wave: 4 bits of
             // I and J each, the first tile lowest
+            static_assert(WAVES == 4, "M's tiles are dealt to four waves");
             const unsigned tiles = wave == 0 ? 0x323130u : wave == 1 ? 0x212033u : wave == 2 ? 0x1022u : 0x0011u;
             const int count = wave < 2 ? 3 : 2;
             for (int n = 0; n < count; ++n) {
@@ -618,8 +711,8 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
                     for (int u = 0; u < CT; ++u) acc[u][I] = mma32(xf[u][s], m, acc[u][I]);
                 }
                 // columns base + 4 NS g .. of token 16 I + l % 16
-                const __bf16* xi = Xs[q] + row_at<LDX>(l16) + base + 4 * NS * g + row_at<LDX>(16 * I);
-                if constexpr (NS == 2) {
+                const __bf16* xi = Xs[q] + row_at<LDX>(l16) + base + 4 * CT * g + row_at<LDX>(16 * I);
+                if constexpr (CT == 2) {
                     const bf16x8 x8 = *reinterpret_cast<const bf16x8*>(xi);
                     bf16x8 out;
 #pragma unroll
@@ -675,17 +768,17 @@ __global__ __launch_bounds__(256, 2) void ssm_scan_bf16_kernel(const SsmArgs a, 
 }
 
 // Joins the kept end states of a sequence in order: slot s becomes the state its segment
-// s + 1 starts from. One thread: four values of one slab.
+// s + 1 starts from. One thread: four values of one slab; one block: K SLAB / JOIN_PARTS.
+constexpr int JOIN_PARTS = 4;
 template <int K>
-__global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, const Plan p) {
-    constexpr int BLOCKS = K * SLAB / 1024;   // blocks a slab
-    const int part = (int)(blockIdx.x % BLOCKS);
-    const int slab = (int)(blockIdx.x / BLOCKS % p.slabs);
-    const long long seq = blockIdx.x / BLOCKS / p.slabs;   // dense: the sequence; packed: a slot
+__global__ __launch_bounds__(K * SLAB / 4 / JOIN_PARTS) void ssm_join_kernel(const SsmArgs a, const Plan p) {
+    const int part = (int)(blockIdx.x % JOIN_PARTS);
+    const int slab = (int)(blockIdx.x / JOIN_PARTS % p.slabs);
+    const long long seq = blockIdx.x / JOIN_PARTS / p.slabs;   // dense: the sequence; packed: a slot
     const Work w = first_pass_work(a.cu_seqlens ? seq : seq * (p.per - 1), a, p);
     if (w.len < 0 || w.s != 0 || w.count <= 2) return;
     const size_t step = (size_t)p.slabs * K * SLAB;
-    float* at = p.ends + ((size_t)w.slot0 * p.slabs + slab) * (size_t)(K * SLAB) + part * 1024 + threadIdx.x * 4;
+    float* at = p.ends + ((size_t)w.slot0 * p.slabs + slab) * (size_t)(K * SLAB) + (part * blockDim.x + threadIdx.x) * 4;
     f32x4 H = *reinterpret_cast<const f32x4*>(at);
     // loads of eight slots at a time are in flight before the first is stored over
     for (int s = 1; s < w.count - 1; s += 8) {
@@ -722,8 +815,8 @@ Plan plan_of(int B, int T, int H, int HV, int K, int V, int N, bool packed, int 
     const long long chunks = (T + C - 1) / C;
     long long seg = chunks > 0 ? chunks : 1;   // chunks of a segment
     if (packed) {
-        // lengths are on the device: bound a long sequence's piece by an even share of the rows
-        const long long share = chunks * p.units / BLOCKS_WANTED;
+        // lengths are on the device: cut what is longer than twice an even share of the rows
+        const long long share = 2 * chunks * p.units / BLOCKS_WANTED;
         const long long piece = share > SEG_MIN ? share : SEG_MIN;
         if (piece < seg) seg = piece;
     } else if ((long long)N * p.units <= 128) {
@@ -739,29 +832,37 @@ Plan plan_of(int B, int T, int H, int HV, int K, int V, int N, bool packed, int 
     p.slots = packed ? (T > p.seg ? (long long)T / p.seg : 0) : (long long)N * (p.per - 1);
     p.ends = p.starts = p.decay = nullptr;
     p.steps = nullptr;
+    p.order = nullptr;
+    p.cuts = nullptr;
     return p;
 }
 
 inline size_t slots_bytes(const Plan& p, int K) { return (size_t)p.slots * p.slabs * K * SLAB * sizeof(float); }
 
+// waves of a two-slab block: the second pass shares its operand reads between two column
+// tiles a wave; the first has half the registers to hold and gains more from eight waves
 template <int K, bool FIRST> void launch_pass(const SsmArgs& a, const Plan& p, unsigned blocks) {
     if (a.dtype == KDA_F32)
         hipLaunchKernelGGL((ssm_scan_f32_kernel<K, FIRST>), dim3(blocks), dim3(256), 0, a.stream, a, p);
     else if (p.ns == 2)
-        hipLaunchKernelGGL((ssm_scan_bf16_kernel<K, 2, FIRST>), dim3(blocks), dim3(256), 0, a.stream, a, p);
+        hipLaunchKernelGGL((ssm_scan_bf16_kernel<K, 2, FIRST ? 8 : 4, FIRST>), dim3(blocks), dim3(FIRST ? 512 : 256), 0, a.stream, a, p);
     else
-        hipLaunchKernelGGL((ssm_scan_bf16_kernel<K, 1, FIRST>), dim3(blocks), dim3(256), 0, a.stream, a, p);
+        hipLaunchKernelGGL((ssm_scan_bf16_kernel<K, 1, 4, FIRST>), dim3(blocks), dim3(256), 0, a.stream, a, p);
 }
 
-// [ends][starts][steps][decay]
+// The workspace: [ends][starts][steps][decay][cuts][order]
 inline size_t steps_bytes(int B, int T, int HV) { return (size_t)3 * HV * B * T * sizeof(float); }
+inline size_t decay_bytes(const Plan& p) { return (size_t)p.slots * p.slabs * sizeof(float); }
+inline size_t order_bytes(const Plan& p, bool packed) { return packed && p.tiles <= ORDER_MAX ? (size_t)p.tiles * sizeof(int) : 0; }
+inline size_t cuts_bytes(const Plan& p, bool packed) { return packed && p.slots > 0 ? sizeof(int) : 0; }
 
 template <int K> hipError_t launch_k(const SsmArgs& a) {
     Plan p = plan_of(a.B, a.T, a.H, a.HV, K, a.V, a.N, a.cu_seqlens != nullptr, a.dtype);
     const long long first = p.slots * p.units, second = p.tiles * p.units;
-    const long long join = p.slots > 0 ? (a.cu_seqlens ? p.slots : (long long)a.N) * p.slabs * (K * SLAB / 1024) : 0;
+    const long long join = p.slots > 0 ? (a.cu_seqlens ? p.slots : (long long)a.N) * p.slabs * JOIN_PARTS : 0;
     const int per = (a.T + C - 1) / C, hblocks = (a.HV + STEP_HEADS - 1) / STEP_HEADS;
-    const long long chunks = (a.cu_seqlens ? (long long)a.T / C + a.N : (long long)a.N * per) * hblocks;
+    const bool packed = a.cu_seqlens != nullptr;
+    const long long chunks = (packed ? (long long)a.T / C + a.N : (long long)a.N * per) * hblocks + 1;
     if (first > 0x7fffffffLL || second > 0x7fffffffLL || join > 0x7fffffffLL || chunks > 0x7fffffffLL)
         return hipErrorInvalidConfiguration;
     char* ws = static_cast<char*>(a.workspace);
@@ -770,17 +871,18 @@ template <int K> hipError_t launch_k(const SsmArgs& a) {
     float* steps = reinterpret_cast<float*>(ws + 2 * slots_bytes(p, K));
     p.steps = steps;
     p.decay = reinterpret_cast<float*>(ws + 2 * slots_bytes(p, K) + steps_bytes(a.B, a.T, a.HV));
-    hipError_t err;
-    if (chunks > 0) {
-        hipLaunchKernelGGL(ssm_steps_kernel, dim3((unsigned)chunks), dim3(256), 0, a.stream, a, steps, per, hblocks);
-        err = hipGetLastError();
-        if (err != hipSuccess) return err;
-    }
+    int* tail = reinterpret_cast<int*>(p.decay + p.slots * p.slabs);
+    if (cuts_bytes(p, packed)) p.cuts = tail++;
+    int* order = order_bytes(p, packed) ? tail : nullptr;
+    p.order = order;
+    hipLaunchKernelGGL(ssm_steps_kernel, dim3((unsigned)chunks), dim3(256), 0, a.stream, a, p, steps, order, per, hblocks);
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
     if (p.slots > 0) {
         launch_pass<K, true>(a, p, (unsigned)first);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
-        hipLaunchKernelGGL((ssm_join_kernel<K>), dim3((unsigned)join), dim3(256), 0, a.stream, a, p);
+        hipLaunchKernelGGL((ssm_join_kernel<K>), dim3((unsigned)join), dim3(K * SLAB / 4 / JOIN_PARTS), 0, a.stream, a, p);
         err = hipGetLastError();
         if (err != hipSuccess) return err;
     }
@@ -792,7 +894,7 @@ template <int K> hipError_t launch_k(const SsmArgs& a) {
 
 size_t ssm_chunk_workspace(int B, int T, int H, int HV, int K, int V, int N, bool packed, int dtype) {
     const Plan p = plan_of(B, T, H, HV, K, V, N, packed, dtype);
-    return 2 * slots_bytes(p, K) + steps_bytes(B, T, HV) + (size_t)p.slots * p.slabs * sizeof(float);
+    return 2 * slots_bytes(p, K) + steps_bytes(B, T, HV) + decay_bytes(p) + cuts_bytes(p, packed) + order_bytes(p, packed);
 }
 
 hipError_t launch_ssm_chunk(const SsmArgs& a) { return a.K == 128 ? launch_k<128>(a) : launch_k<64>(a); }

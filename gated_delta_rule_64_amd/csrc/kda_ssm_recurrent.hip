@@ -55,7 +55,7 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmArgs a, int
 #pragma unroll
         for (int i = 0; i < R; ++i) S[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    const float A_log = a.A_log[hv];
+    const double rate = ssm_rate(a.A_log[hv]);
     const float bias = a.dt_bias ? a.dt_bias[hv] : 0.f;
     const float skip = a.D ? a.D[hv] : 0.f;
     for (int t = bos; t < eos; ++t) {
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256) void ssm_recurrent_kernel(const SsmArgs a, int
         load_rows<RG, R, false>(static_cast<const TIn*>(a.c) + r * a.c_stride + (size_t)h * K, rg, cc);
         load4(static_cast<const TIn*>(a.x) + r * a.x_stride + (size_t)hv * a.V + c0, xx);
         const float dt = ssm_step(load_scalar(a.dt, a.dt_dtype, r * a.dt_stride + hv), bias, a.softplus);
-        const float keep = exp2_fast((float)ssm_log2_decay(dt, A_log));
+        const float keep = exp2_fast((float)ssm_log2_decay(dt, rate));
         float p[4] = {0.f, 0.f, 0.f, 0.f}, u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[j] = dt * xx[j];
