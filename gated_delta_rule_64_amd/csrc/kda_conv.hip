@@ -16,8 +16,10 @@ namespace kda {
 
 namespace {
 
-constexpr int TT_FWD = 16;
+// Rows are taken R at a time, the next R in flight while these are worked on.
+constexpr int TT_FWD = 32;
 constexpr int TT_BWD = 32;
+constexpr int R = 4;
 
 // lanes of a block along the channels (a power of two, at most 64); the block's other lanes
 // take other tiles
@@ -28,13 +30,36 @@ inline int lanes_along(int D, int vec) {
     return l;
 }
 
-template <typename T, int VEC, int W>
+// VEC elements of a row as they are stored
+template <typename T, int VEC> struct Raw { typedef __attribute__((ext_vector_type(VEC))) T type; };
+template <typename T> struct Raw<T, 1> { typedef T type; };
+template <typename T, int VEC> __device__ __forceinline__ typename Raw<T, VEC>::type load_raw(const T* p) {
+    return *reinterpret_cast<const typename Raw<T, VEC>::type*>(p);
+}
+template <typename T, int VEC> __device__ __forceinline__ void widen(const typename Raw<T, VEC>::type& v, float (&o)[VEC]) {
+    if constexpr (VEC == 1) {
+        o[0] = (float)v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = (float)v[e];
+    }
+}
+
+// The taps and bias of channels d .. d + VEC - 1: VEC W contiguous weights.
+template <int VEC, int W>
 __device__ __forceinline__ void load_taps(const ConvArgs& a, int d, float (&w)[W][VEC], float (&bias)[VEC]) {
+    float flat[W][VEC];   // piece by piece of the [VEC][W] block
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
+    for (int i = 0; i < W; ++i) load_param<VEC>(a.weight, a.w_dtype, (long long)d * W + i * VEC, flat[i]);
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[i][e] = load_scalar(a.weight, a.w_dtype, (long long)(d + e) * W + i);
-        bias[e] = a.bias ? load_scalar(a.bias, a.w_dtype, d + e) : 0.f;
+    for (int e = 0; e < VEC; ++e)
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i][e] = flat[(e * W + i) / VEC][(e * W + i) % VEC];
+    if (a.bias) {
+        load_param<VEC>(a.bias, a.w_dtype, d, bias);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) bias[e] = 0.f;
     }
 }
 
@@ -61,9 +86,19 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvArgs a, int alo
     if (d >= a.D || tile >= tiles) return;
     const SeqTile s = seq_tile(tile, a.cu_seqlens, a.N, a.T, TT_FWD, tiles_dense);
     if (s.len < 0) return;
+    const int end = s.len - s.pos < TT_FWD ? s.len - s.pos : TT_FWD;
+    const T* xp = static_cast<const T*>(a.x) + (s.row0 + s.pos) * a.x_stride + d;
+    T* yp = static_cast<T*>(a.y) + (s.row0 + s.pos) * (long long)a.D + d;
 
-    float w[W][VEC], bias[VEC], win[W][VEC];
-    load_taps<T, VEC, W>(a, d, w, bias);
+    // past the tile the last row stands in
+    typename Raw<T, VEC>::type cur[R], next[R];
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) next[k] = load_raw<T, VEC>(xp + (long long)min(t0 + k, end - 1) * a.x_stride);
+    };
+    if (end > 0) fetch(0);
+    float w[W][VEC], bias[VEC], win[W - 1 + R][VEC];
+    load_taps<VEC, W>(a, d, w, bias);
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) load_row<T, VEC, W>(a, s, s.pos - (W - 1) + i, d, win[i]);
 
@@ -77,25 +112,27 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvArgs a, int alo
         for (int j = 0; j < W - 1; ++j)
             store_vec<VEC>(static_cast<T*>(a.final_state) + ((long long)s.n * (W - 1) + j) * a.D + d, last[j]);
     }
-    const int end = s.len - s.pos < TT_FWD ? s.len - s.pos : TT_FWD;
-    const T* xp = static_cast<const T*>(a.x) + (s.row0 + s.pos) * a.x_stride + d;
-    T* yp = static_cast<T*>(a.y) + (s.row0 + s.pos) * (long long)a.D + d;
-#pragma unroll 4
-    for (int t = 0; t < end; ++t) {
-        load_vec<VEC>(xp + t * a.x_stride, win[W - 1]);
-        float out[VEC];
+    for (int t0 = 0; t0 < end; t0 += R) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float acc = bias[e];
+        for (int k = 0; k < R; ++k) cur[k] = next[k];
+        if (t0 + R < end) fetch(t0 + R);
 #pragma unroll
-            for (int i = 0; i < W; ++i) acc = fmaf(w[i][e], win[i][e], acc);
-            out[e] = a.silu ? acc * sigmoid_fast(acc) : acc;
+        for (int k = 0; k < R; ++k) {
+            widen<T, VEC>(cur[k], win[W - 1 + k]);
+            float out[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float acc = bias[e];
+#pragma unroll
+                for (int i = 0; i < W; ++i) acc = fmaf(w[i][e], win[k + i][e], acc);
+                out[e] = a.silu ? acc * sigmoid_fast(acc) : acc;
+            }
+            if (t0 + k < end) store_vec<VEC>(yp + (long long)(t0 + k) * a.D, out);
         }
-        store_vec<VEC>(yp + (long long)t * a.D, out);
 #pragma unroll
         for (int i = 0; i < W - 1; ++i)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) win[i][e] = win[i + 1][e];
+            for (int e = 0; e < VEC; ++e) win[i][e] = win[R + i][e];
     }
 }
 
@@ -104,7 +141,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvArgs a, int alo
 // t is one of its own rows, dw[i] += dpre[t] x[t - (W-1) + i] and db += dpre[t] in fp32.
 // The sequence's first tile also has the state's rows (positions -(W-1) .. -1).
 // The block adds its tiles' sums in LDS and leaves one row of partial sums; sum_rows adds
-// those in order, so results do not depend on scheduling.
+// those in order, so results do not depend on scheduling. A lane has four channels here (8
+// bytes of bf16): with eight, the two windows and the sums take 250 registers.
 template <typename T, int VEC, int W>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int along, int dblocks, long long tiles,
                                                        int tiles_dense, long long P) {
@@ -122,74 +160,95 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
 #pragma unroll
         for (int i = 0; i < W; ++i) dw[i][e] = 0.f;
     }
-    if (live) load_taps<T, VEC, W>(a, d, w, bias);
+    if (live) load_taps<VEC, W>(a, d, w, bias);
     for (long long tile = p * groups + grp; live && tile < tiles; tile += P * groups) {
         const SeqTile s = seq_tile(tile, a.cu_seqlens, a.N, a.T, TT_BWD, tiles_dense);
         if (s.len < 0) continue;
         const int end = s.len - s.pos < TT_BWD ? s.len : s.pos + TT_BWD;   // own rows: s.pos .. end-1
         const int first = s.pos == 0 ? -(W - 1) : s.pos;                   // rows whose gradient is written
-        float win[W][VEC], dp[W][VEC];                                    // x and dpre, the last W rows
+        const T* xp = static_cast<const T*>(a.x) + s.row0 * a.x_stride + d;
+        const T* yp = static_cast<const T*>(b.dy) + s.row0 * (long long)a.D + d;
+        // past the sequence the last row stands in, its dpre taken as 0
+        typename Raw<T, VEC>::type cx[R], cy[R], nx[R], ny[R];
+        auto fetch = [&](int t0) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const long long t = min(t0 + k, s.len - 1);
+                nx[k] = load_raw<T, VEC>(xp + t * a.x_stride);
+                ny[k] = load_raw<T, VEC>(yp + t * a.D);
+            }
+        };
+        if (s.len > 0) fetch(s.pos);
+        float win[W - 1 + R][VEC], dp[W - 1 + R][VEC];   // x and dpre, the last rows and these
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) load_row<T, VEC, W>(a, s, s.pos - (W - 1) + i, d, win[i]);
 #pragma unroll
-        for (int i = 0; i < W; ++i)
+        for (int i = 0; i < W - 1; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) dp[i][e] = 0.f;
-        for (int t = s.pos; t < end + W - 1; ++t) {
-            // dpre of row t (zero past the sequence)
-            if (t < s.len) {
-                load_row<T, VEC, W>(a, s, t, d, win[W - 1]);
-                load_vec<VEC>(static_cast<const T*>(b.dy) + (s.row0 + t) * (long long)a.D + d, dp[W - 1]);
-                if (a.silu) {
+        for (int t0 = s.pos; t0 < end + W - 1; t0 += R) {
+            if (s.len > 0) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
+                for (int k = 0; k < R; ++k) {
+                    cx[k] = nx[k];
+                    cy[k] = ny[k];
+                }
+                if (t0 + R < end + W - 1) fetch(t0 + R);
+            }
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int t = t0 + k;
+                if (s.len > 0) {
+                    widen<T, VEC>(cx[k], win[W - 1 + k]);
+                    widen<T, VEC>(cy[k], dp[W - 1 + k]);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    float g = dp[W - 1 + k][e];
+                    if (a.silu) {
                         float acc = bias[e];
 #pragma unroll
-                        for (int i = 0; i < W; ++i) acc = fmaf(w[i][e], win[i][e], acc);
+                        for (int i = 0; i < W; ++i) acc = fmaf(w[i][e], win[k + i][e], acc);
                         const float sg = sigmoid_fast(acc);
-                        dp[W - 1][e] *= sg * (1.f + acc * (1.f - sg));
+                        g *= sg * (1.f + acc * (1.f - sg));
+                    }
+                    g = t < s.len ? g : 0.f;
+                    dp[W - 1 + k][e] = g;
+                    if (t < end) {
+                        db[e] += g;
+#pragma unroll
+                        for (int i = 0; i < W; ++i) dw[i][e] = fmaf(g, win[k + i][e], dw[i][e]);
                     }
                 }
-            } else {
+                // row t - (W-1) has every term: dpre[t - (W-1) .. t] against w[W-1 .. 0]
+                const int r = t - (W - 1);
+                if (r >= first && r < end) {
+                    float g[VEC];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) dp[W - 1][e] = 0.f;
-            }
-            if (t < end) {
+                    for (int e = 0; e < VEC; ++e) {
+                        g[e] = 0.f;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    db[e] += dp[W - 1][e];
+                        for (int i = 0; i < W; ++i) g[e] = fmaf(w[W - 1 - i][e], dp[k + i][e], g[e]);
+                    }
+                    const int j = r - (s.len - (W - 1));   // the row of the final state it is handed on as
+                    if (b.dfinal && j >= 0) {
+                        float f[VEC];
+                        load_vec<VEC>(static_cast<const T*>(b.dfinal) + ((long long)s.n * (W - 1) + j) * a.D + d, f);
 #pragma unroll
-                    for (int i = 0; i < W; ++i) dw[i][e] = fmaf(dp[W - 1][e], win[i][e], dw[i][e]);
+                        for (int e = 0; e < VEC; ++e) g[e] += f[e];
+                    }
+                    if (r >= 0)
+                        store_vec<VEC>(static_cast<T*>(b.dx) + (s.row0 + r) * (long long)a.D + d, g);
+                    else if (b.dinitial)
+                        store_vec<VEC>(static_cast<T*>(b.dinitial) + ((long long)s.n * (W - 1) + W - 1 + r) * a.D + d, g);
                 }
-            }
-            // row t - (W-1) has every term: dpre[t - (W-1) .. t] against w[W-1 .. 0]
-            const int r = t - (W - 1);
-            if (r >= first) {
-                float g[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    g[e] = 0.f;
-#pragma unroll
-                    for (int i = 0; i < W; ++i) g[e] = fmaf(w[W - 1 - i][e], dp[i][e], g[e]);
-                }
-                const int j = r - (s.len - (W - 1));   // the row of the final state it is handed on as
-                if (b.dfinal && j >= 0) {
-                    float f[VEC];
-                    load_vec<VEC>(static_cast<const T*>(b.dfinal) + ((long long)s.n * (W - 1) + j) * a.D + d, f);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) g[e] += f[e];
-                }
-                if (r >= 0)
-                    store_vec<VEC>(static_cast<T*>(b.dx) + (s.row0 + r) * (long long)a.D + d, g);
-                else if (b.dinitial)
-                    store_vec<VEC>(static_cast<T*>(b.dinitial) + ((long long)s.n * (W - 1) + W - 1 + r) * a.D + d, g);
             }
 #pragma unroll
             for (int i = 0; i < W - 1; ++i)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    win[i][e] = win[i + 1][e];
-                    dp[i][e] = dp[i + 1][e];
+                    win[i][e] = win[R + i][e];
+                    dp[i][e] = dp[R + i][e];
                 }
         }
     }
@@ -236,11 +295,13 @@ inline long long tiles_of(int B, int T, int N, bool packed, int TT) {
 }
 inline int tiles_dense_of(int T, int TT) { return (T + TT - 1) / TT > 0 ? (T + TT - 1) / TT : 1; }
 
-// blocks along the rows of the backward: enough blocks to fill the chip, few partial sums
-inline long long bwd_rows_of_blocks(long long tiles, int groups, int dblocks) {
+// blocks along the rows of the backward, one row of partial sums each: up to 128, then even
+// rounds of them
+inline long long bwd_rows_of_blocks(long long tiles, int groups) {
     const long long most = (tiles + groups - 1) / groups;
-    long long want = (1024 + dblocks - 1) / dblocks;
-    return most < want ? (most > 0 ? most : 1) : want;
+    if (most <= 128) return most > 0 ? most : 1;
+    const long long rounds = (most + 127) / 128;
+    return (most + rounds - 1) / rounds;
 }
 
 template <typename T, int VEC>
@@ -267,7 +328,7 @@ hipError_t bwd_v(const ConvBwdArgs& b) {
     const int dblocks = (a.D + along * VEC - 1) / (along * VEC);
     const long long tiles = tiles_of(a.B, a.T, a.N, a.cu_seqlens != nullptr, TT_BWD);
     const int groups = 256 / along;
-    const long long P = bwd_rows_of_blocks(tiles, groups, dblocks);
+    const long long P = bwd_rows_of_blocks(tiles, groups);
     const long long blocks = P * dblocks;
     if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
     const int td = tiles_dense_of(a.T, TT_BWD);
@@ -291,13 +352,11 @@ hipError_t launch_sum_rows(const SumRows& s, hipStream_t stream) {
     return hipGetLastError();
 }
 
-long long conv_bwd_partials(int B, int T, int D, int N, bool packed, int dtype) {
+long long conv_bwd_partials(int B, int T, int D, int N, bool packed) {
     // the scalar and the 16-byte form differ in their blocks: room for either
     long long most = 0;
-    for (int vec : {1, dtype == KDA_BF16 ? 8 : 4}) {
-        const int along = lanes_along(D, vec);
-        const int dblocks = (D + along * vec - 1) / (along * vec);
-        const long long P = bwd_rows_of_blocks(tiles_of(B, T, N, packed, TT_BWD), 256 / along, dblocks);
+    for (int vec : {1, 4}) {
+        const long long P = bwd_rows_of_blocks(tiles_of(B, T, N, packed, TT_BWD), 256 / lanes_along(D, vec));
         most = P > most ? P : most;
     }
     return most;
@@ -311,7 +370,7 @@ hipError_t launch_conv_fwd(const ConvArgs& a) {
 
 hipError_t launch_conv_bwd(const ConvBwdArgs& b) {
     const bool wide = b.f.wide;
-    if (b.f.dtype == KDA_BF16) return wide ? bwd_v<__bf16, 8>(b) : bwd_v<__bf16, 1>(b);
+    if (b.f.dtype == KDA_BF16) return wide ? bwd_v<__bf16, 4>(b) : bwd_v<__bf16, 1>(b);
     return wide ? bwd_v<float, 4>(b) : bwd_v<float, 1>(b);
 }
 

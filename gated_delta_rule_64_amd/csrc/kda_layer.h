@@ -88,7 +88,7 @@ struct SsmArgs {
 
 hipError_t launch_conv_fwd(const ConvArgs& a);
 hipError_t launch_conv_bwd(const ConvBwdArgs& a);
-long long conv_bwd_partials(int B, int T, int D, int N, bool packed, int dtype);
+long long conv_bwd_partials(int B, int T, int D, int N, bool packed);
 // whether a row of D values can be moved 16 bytes at a time
 inline bool rows_of_16_bytes(int dtype, int D, long long stride) {
     const int vec = dtype == KDA_BF16 ? 8 : 4;

@@ -68,13 +68,13 @@ int conv_args(kda::ConvArgs* a, const void* x, long long x_stride, const void* w
     a->y = nullptr; a->final_state = nullptr;
     a->N = N; a->B = B; a->T = T; a->D = D; a->W = W;
     a->dtype = dtype; a->w_dtype = w_dtype; a->silu = activation == KDA_ACT_SILU;
-    a->wide = kda::rows_of_16_bytes(dtype, D, x_stride) && all_aligned16(x, initial_state);
+    a->wide = kda::rows_of_16_bytes(dtype, D, x_stride) && all_aligned16(x, initial_state, weight, bias);
     a->dev_status = dev_status; a->stream = stream;
     return KDA_OK;
 }
 
-size_t conv_bwd_need(int B, int T, int D, int W, int N, bool packed, int dtype) {
-    return (size_t)kda::conv_bwd_partials(B, T, D, N, packed, dtype) * (size_t)(W + 1) * (size_t)D * sizeof(float);
+size_t conv_bwd_need(int B, int T, int D, int W, int N, bool packed) {
+    return (size_t)kda::conv_bwd_partials(B, T, D, N, packed) * (size_t)(W + 1) * (size_t)D * sizeof(float);
 }
 
 int ssm_args(kda::SsmArgs* a, const void* x, long long x_stride, const void* dt, long long dt_stride,
@@ -164,7 +164,7 @@ int kda_conv_fwd(const void* x, long long x_stride, const void* weight, const vo
 
 size_t kda_conv_bwd_workspace_bytes(int B, int T, int D, int W, int N, int packed, int dtype) {
     if (B < 0 || T < 0 || N < 0 || D <= 0 || D > (1 << 28) || W < 2 || W > 4 || !is_dtype(dtype)) return 0;
-    return conv_bwd_need(B, T, D, W, packed ? N : B, packed != 0, dtype);
+    return conv_bwd_need(B, T, D, W, packed ? N : B, packed != 0);
 }
 
 int kda_conv_bwd(const void* dy, const void* x, long long x_stride, const void* weight, const void* bias,
@@ -177,7 +177,7 @@ int kda_conv_bwd(const void* dy, const void* x, long long x_stride, const void* 
         return rc;
     if ((long long)B * T > 0 && (!dy || !dx)) return set_error(KDA_ERR_NULL, "dy and dx must be non-NULL");
     if (!dweight || !weight) return set_error(KDA_ERR_NULL, "weight and dweight must be non-NULL");
-    if (int rc = check_workspace(workspace, workspace_bytes, conv_bwd_need(B, T, D, W, N, cu_seqlens != nullptr, dtype), 16))
+    if (int rc = check_workspace(workspace, workspace_bytes, conv_bwd_need(B, T, D, W, N, cu_seqlens != nullptr), 16))
         return rc;
     b.dy = dy; b.dfinal = dfinal; b.dx = dx; b.dweight = dweight; b.dbias = dbias; b.dinitial = dinitial;
     b.partial = static_cast<float*>(workspace);
