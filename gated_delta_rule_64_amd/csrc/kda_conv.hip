@@ -16,10 +16,13 @@ namespace kda {
 
 namespace {
 
-// Rows are taken R at a time, the next R in flight while these are worked on.
+// Rows are taken R (backward: RB) at a time, the next ones in flight while these are worked
+// on. Backward of 2 x 4096 rows x 6144 channels: RB 2 and tiles of 64 rows 99 us, 2 and 32
+// 106, 4 and 32 121, 4 and 64 140 (more rows at once take registers the waves lack).
 constexpr int TT_FWD = 32;
-constexpr int TT_BWD = 32;
+constexpr int TT_BWD = 64;
 constexpr int R = 4;
+constexpr int RB = 2;
 
 // lanes of a block along the channels (a power of two, at most 64); the block's other lanes
 // take other tiles
@@ -169,34 +172,34 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
         const T* xp = static_cast<const T*>(a.x) + s.row0 * a.x_stride + d;
         const T* yp = static_cast<const T*>(b.dy) + s.row0 * (long long)a.D + d;
         // past the sequence the last row stands in, its dpre taken as 0
-        typename Raw<T, VEC>::type cx[R], cy[R], nx[R], ny[R];
+        typename Raw<T, VEC>::type cx[RB], cy[RB], nx[RB], ny[RB];
         auto fetch = [&](int t0) {
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
+            for (int k = 0; k < RB; ++k) {
                 const long long t = min(t0 + k, s.len - 1);
                 nx[k] = load_raw<T, VEC>(xp + t * a.x_stride);
                 ny[k] = load_raw<T, VEC>(yp + t * a.D);
             }
         };
         if (s.len > 0) fetch(s.pos);
-        float win[W - 1 + R][VEC], dp[W - 1 + R][VEC];   // x and dpre, the last rows and these
+        float win[W - 1 + RB][VEC], dp[W - 1 + RB][VEC];   // x and dpre, the last rows and these
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) load_row<T, VEC, W>(a, s, s.pos - (W - 1) + i, d, win[i]);
 #pragma unroll
         for (int i = 0; i < W - 1; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) dp[i][e] = 0.f;
-        for (int t0 = s.pos; t0 < end + W - 1; t0 += R) {
+        for (int t0 = s.pos; t0 < end + W - 1; t0 += RB) {
             if (s.len > 0) {
 #pragma unroll
-                for (int k = 0; k < R; ++k) {
+                for (int k = 0; k < RB; ++k) {
                     cx[k] = nx[k];
                     cy[k] = ny[k];
                 }
-                if (t0 + R < end + W - 1) fetch(t0 + R);
+                if (t0 + RB < end + W - 1) fetch(t0 + RB);
             }
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
+            for (int k = 0; k < RB; ++k) {
                 const int t = t0 + k;
                 if (s.len > 0) {
                     widen<T, VEC>(cx[k], win[W - 1 + k]);
@@ -247,8 +250,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
             for (int i = 0; i < W - 1; ++i)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
-                    win[i][e] = win[R + i][e];
-                    dp[i][e] = dp[R + i][e];
+                    win[i][e] = win[RB + i][e];
+                    dp[i][e] = dp[RB + i][e];
                 }
         }
     }
@@ -267,14 +270,15 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
     }
 }
 
-// Sums of P rows of M partial sums: 64 columns x 4 quarters of the rows per block.
-__global__ __launch_bounds__(256) void sum_rows_kernel(const SumRows s) {
-    __shared__ float part[4][64];
-    const int ln = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const long long m = (long long)blockIdx.x * 64 + ln;
+// Sums of P rows of M partial sums: a block takes 32 columns, 32 groups of the rows each,
+// and adds the groups in order.
+__global__ __launch_bounds__(1024) void sum_rows_kernel(const SumRows s) {
+    __shared__ float part[32][33];
+    const int ln = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const long long m = (long long)blockIdx.x * 32 + ln;
     float acc = 0.f;
     if (m < s.M) {
-        const long long each = (s.P + 3) / 4;
+        const long long each = (s.P + 31) / 32;
         const long long p0 = q * each, p1 = p0 + each < s.P ? p0 + each : s.P;
 #pragma unroll 8
         for (long long p = p0; p < p1; ++p) acc += s.part[p * s.M + m];
@@ -282,7 +286,8 @@ __global__ __launch_bounds__(256) void sum_rows_kernel(const SumRows s) {
     part[q][ln] = acc;
     __syncthreads();
     if (q != 0 || m >= s.M) return;
-    acc = (part[0][ln] + part[1][ln]) + (part[2][ln] + part[3][ln]);
+#pragma unroll
+    for (int k = 1; k < 32; ++k) acc += part[k][ln];
     const long long row = m / s.D;
     const int d = (int)(m % s.D);
     if (row < s.taps) s.out[(long long)d * s.taps + row] = acc;
@@ -348,7 +353,7 @@ hipError_t bwd_v(const ConvBwdArgs& b) {
 }  // namespace
 
 hipError_t launch_sum_rows(const SumRows& s, hipStream_t stream) {
-    hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((s.M + 63) / 64)), dim3(256), 0, stream, s);
+    hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((s.M + 31) / 32)), dim3(1024), 0, stream, s);
     return hipGetLastError();
 }
 
