@@ -56,13 +56,18 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (2 us of an 11 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(dev, fn, *args):
     """``fn(*args, stream)`` on ``dev``'s current stream, with ``dev`` current."""
     if dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        rc = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, _raw_stream(dev.index))
     if rc != 0:
         raise KdaError(rc, _lib.kda_last_error())
 
@@ -72,13 +77,14 @@ def _want(name, t, shape, dtypes, dev=None):
     contiguous and there."""
     if t is None:
         return
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: got shape {tuple(t.shape)}, this problem needs {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: got shape {tuple(t.shape)}, this problem needs {tuple(shape)}")
     if t.dtype not in dtypes:
         names = " or ".join(str(d).replace("torch.", "") for d in dtypes)
         raise TypeError(f"{name}: got dtype {str(t.dtype).replace('torch.', '')}, expected {names}")
     if dev is not None:
-        _placed(name, t, dev)
+        if t.device != dev or not t.is_cuda:
+            _placed(name, t, dev)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
@@ -97,24 +103,29 @@ _F32 = (torch.float32,)
 def _row_stride(name, t, lead):
     """Elements between consecutive rows of ``t``, whose first ``lead`` axes count rows and
     whose others are a row, contiguous inside; the rows evenly spaced."""
+    shape = t.shape
     width = 1
-    for d in range(t.dim() - 1, lead - 1, -1):
-        if t.shape[d] != 1 and t.stride(d) != width:
-            raise ValueError(f"{name}: the elements of a row must be contiguous")
-        width *= t.shape[d]
-    if t.numel() == 0:
+    for n in shape[lead:]:
+        width *= n
+    if t.is_contiguous():
         return width
+    strides = t.stride()
+    inner = 1
+    for n, step in zip(shape[:lead - 1:-1], strides[:lead - 1:-1]):
+        if n != 1 and step != inner:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        inner *= n
     stride, span = None, None
-    for d in range(lead - 1, -1, -1):
-        n = t.shape[d]
+    for n, step in zip(shape[lead - 1::-1], strides[lead - 1::-1]):
         if n == 1:
             continue
         if stride is None:
-            stride = t.stride(d)
-        elif t.stride(d) != span:
+            stride = step
+        elif step != span:
             raise ValueError(f"{name}: rows must be evenly spaced over the leading axes")
-        span = t.stride(d) * n
-    stride = width if stride is None else stride
+        span = step * n
+    if stride is None:
+        return width
     if stride < width:
         raise ValueError(f"{name}: rows must not overlap")
     return stride

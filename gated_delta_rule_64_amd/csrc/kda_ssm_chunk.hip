@@ -323,7 +323,8 @@ template <int K, bool FIRST>
 __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, const Plan p) {
     constexpr int KT = K / 16;
     constexpr int LDB = K + PAD, LDX = SLAB + PAD;
-    __shared__ float Bs[C * LDB], Cs[FIRST ? 1 : C * LDB], Xs[C * LDX];
+    constexpr int NB = C * K / 4 / 256, NX = C * SLAB / 4 / 256;   // 16-byte pieces a thread
+    __shared__ __attribute__((aligned(16))) float Bs[C * LDB], Cs[FIRST ? 1 : C * LDB], Xs[C * LDX];
     __shared__ f32x4 Ms[FIRST ? 1 : 10 * 64];   // M^T tiles (I, J <= I) in accumulator order
     __shared__ Steps st;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -345,21 +346,34 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
         const int cl = w.len - p0 < C ? w.len - p0 : C;
         const long long row = w.row0 + p0;
         __syncthreads();   // the last chunk's readers are done
-        for (int i = threadIdx.x; i < C * K / 4; i += 256) {
-            const int t = i / (K / 4), k = i % (K / 4) * 4;
-            float u[4] = {0.f, 0.f, 0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (t < cl) {
-                load_vec<4>(static_cast<const float*>(a.b) + (row + t) * a.b_stride + (size_t)h * K + k, u);
-                if (!FIRST) load_vec<4>(static_cast<const float*>(a.c) + (row + t) * a.c_stride + (size_t)h * K + k, v);
+        // all of the chunk's loads in flight before the first is stored
+        f32x4 rb[NB], rc[FIRST ? 1 : NB], rx[NX];
+        const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int e = i * 256 + threadIdx.x, t = e / (K / 4), k = e % (K / 4) * 4;
+            const float* at = static_cast<const float*>(a.b) + (row + min(t, cl - 1)) * a.b_stride + (size_t)h * K + k;
+            rb[i] = *reinterpret_cast<const f32x4*>(at);
+            if constexpr (!FIRST) {
+                const float* ct = static_cast<const float*>(a.c) + (row + min(t, cl - 1)) * a.c_stride + (size_t)h * K + k;
+                rc[i] = *reinterpret_cast<const f32x4*>(ct);
             }
-            store_vec<4>(Bs + t * LDB + k, u);
-            if (!FIRST) store_vec<4>(Cs + t * LDB + k, v);
         }
-        for (int i = threadIdx.x; i < C * SLAB / 4; i += 256) {
-            const int t = i / (SLAB / 4), q = i % (SLAB / 4) * 4;
-            float u[4] = {0.f, 0.f, 0.f, 0.f};
-            if (t < cl) load_vec<4>(static_cast<const float*>(a.x) + (row + t) * a.x_stride + (size_t)slab * SLAB + q, u);
-            store_vec<4>(Xs + t * LDX + q, u);
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int e = i * 256 + threadIdx.x, t = e / (SLAB / 4), k = e % (SLAB / 4) * 4;
+            rx[i] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.x) + (row + min(t, cl - 1)) * a.x_stride + (size_t)slab * SLAB + k);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int e = i * 256 + threadIdx.x, t = e / (K / 4), k = e % (K / 4) * 4;
+            *reinterpret_cast<f32x4*>(Bs + t * LDB + k) = t < cl ? rb[i] : none;
+            if constexpr (!FIRST) *reinterpret_cast<f32x4*>(Cs + t * LDB + k) = t < cl ? rc[i] : none;
+        }
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int e = i * 256 + threadIdx.x, t = e / (SLAB / 4), k = e % (SLAB / 4) * 4;
+            *reinterpret_cast<f32x4*>(Xs + t * LDX + k) = t < cl ? rx[i] : none;
         }
         if (wave == 0) total += place_steps(load_step(a, p, row, cl, hv), cl, &st);
         __syncthreads();
