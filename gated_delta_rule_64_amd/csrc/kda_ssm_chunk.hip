@@ -494,9 +494,14 @@ template <int LD> __device__ __forceinline__ bf16x4 read_col4(const __bf16* t, i
     return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(t + row_at<LD>(16 * J))));
 }
 __device__ __forceinline__ bf16x8 join(bf16x4 u, bf16x4 v) { return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7); }
-// a row's 32 elements of step s, in accumulator order: 4 g .. +3 of both halves
+// a row's 32 elements of step s, in accumulator order: 4 g .. +3 of both halves. Volatile, so
+// that the compiler does not pair the reads: a ds_read2_b64 on this layout takes 16 cycles of
+// LDS, half of them conflicts, where two ds_read_b64 take 4 (scan of 8192 tokens x 32 heads
+// 121 us with pairs, 116 without).
 __device__ __forceinline__ bf16x8 read_row(const __bf16* row, int s) {
-    return join(*reinterpret_cast<const bf16x4*>(row + 32 * s), *reinterpret_cast<const bf16x4*>(row + 32 * s + 16));
+    typedef volatile __attribute__((address_space(3))) const bf16x4* lds;
+    const bf16x4 u = *(lds)(row + 32 * s), v = *(lds)(row + 32 * s + 16);
+    return join(u, v);
 }
 // elements e and e + 1 of x times their weights, each cut into three bf16 whose sum is the
 // fp32 product exactly (8 + 8 + 8 bits, by truncation)
@@ -784,6 +789,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
 // Joins the kept end states of a sequence in order: slot s becomes the state its segment
 // s + 1 starts from. One thread: four values of one slab; one block: K SLAB / JOIN_PARTS.
 constexpr int JOIN_PARTS = 4;
+constexpr int BATCH = 8;
 template <int K>
 __global__ __launch_bounds__(K * SLAB / 4 / JOIN_PARTS) void ssm_join_kernel(const SsmArgs a, const Plan p) {
     const int part = (int)(blockIdx.x % JOIN_PARTS);
@@ -795,24 +801,24 @@ __global__ __launch_bounds__(K * SLAB / 4 / JOIN_PARTS) void ssm_join_kernel(con
     float* at = p.ends + ((size_t)w.slot0 * p.slabs + slab) * (size_t)(K * SLAB) + (part * blockDim.x + threadIdx.x) * 4;
     f32x4 H = *reinterpret_cast<const f32x4*>(at);
     // loads of eight slots at a time are in flight before the first is stored over
-    for (int s = 1; s < w.count - 1; s += 8) {
-        const int m = min(8, w.count - 1 - s);
-        f32x4 L[8];
-        float d[8];
+    for (int s = 1; s < w.count - 1; s += BATCH) {
+        const int m = min(BATCH, w.count - 1 - s);
+        f32x4 L[BATCH];
+        float d[BATCH];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             const int k = i < m ? i : 0;
             L[i] = *reinterpret_cast<const f32x4*>(at + (k + 1) * step);
             d[i] = p.decay[(w.slot0 + s + k) * p.slabs + slab];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             if (i >= m) break;
 #pragma unroll
             for (int r = 0; r < 4; ++r) H[r] = fmaf(d[i], H[r], L[i][r]);
             *reinterpret_cast<f32x4*>(at + (i + 1) * step) = H;
         }
-        at += 8 * step;
+        at += BATCH * step;
     }
 }
 
