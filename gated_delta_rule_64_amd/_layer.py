@@ -111,19 +111,19 @@ def _row_stride(name, t, lead):
         return width
     strides = t.stride()
     inner = 1
-    for n, step in zip(shape[:lead - 1:-1], strides[:lead - 1:-1]):
-        if n != 1 and step != inner:
+    for d in range(len(shape) - 1, lead - 1, -1):
+        if shape[d] != 1 and strides[d] != inner:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
-        inner *= n
+        inner *= shape[d]
     stride, span = None, None
-    for n, step in zip(shape[lead - 1::-1], strides[lead - 1::-1]):
-        if n == 1:
+    for d in range(lead - 1, -1, -1):
+        if shape[d] == 1:
             continue
         if stride is None:
-            stride = step
-        elif step != span:
+            stride = strides[d]
+        elif strides[d] != span:
             raise ValueError(f"{name}: rows must be evenly spaced over the leading axes")
-        span = step * n
+        span = strides[d] * shape[d]
     if stride is None:
         return width
     if stride < width:
@@ -163,6 +163,13 @@ def _bytes(name, workspace, need, dev):
     if not workspace.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return workspace
+
+
+def _apart(name, out, inputs):
+    """An output a caller gives is none of the inputs that are read after it is written."""
+    for other, t in inputs:
+        if t is not None and out.data_ptr() == t.data_ptr() and out.numel():
+            raise ValueError(f"{name} must not be {other}")
 
 
 def _size(t):
@@ -207,6 +214,7 @@ def kda_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, outp
         out = torch.empty(B, T, D, dtype=x.dtype, device=dev)
     else:
         _want("out", out, (B, T, D), (x.dtype,), dev)
+        _apart("out", out, (("x", x), ("initial_state", initial_state)))
     if not output_final_state:
         final_state = None
     elif final_state is None:
@@ -276,6 +284,7 @@ def _ssm(chunk, x, dt, A_log, b, c, D, dt_bias, initial_state, cu_seqlens, outpu
         out = torch.empty(B, T, HV, V, dtype=x.dtype, device=dev)
     else:
         _want("out", out, (B, T, HV, V), (x.dtype,), dev)
+        _apart("out", out, (("x", x), ("b", b), ("c", c), ("dt", dt)))
     if not output_final_state:
         final_state = None
     elif final_state is None:

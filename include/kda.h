@@ -402,6 +402,11 @@ size_t kda_noalloc_scratch_bytes(void);
  *   - dtype is KDA_BF16 or KDA_F32 for the activations; arithmetic, sums and states are fp32.
  *   - A NaN or infinity in a token never reaches another sequence. kda_ssm_chunk_fwd may let
  *     it reach earlier outputs of its own 64-token chunk (0 times NaN in a matrix product).
+ *   - No output may overlap an input, except where that is said.
+ *   - kda_conv_fwd, kda_conv_bwd and kda_ssm_chunk_fwd find a packed batch's tiles by searching
+ *     the offsets. Where a slot's offsets are broken, that slot is skipped and flagged as
+ *     everywhere; the other slots' outputs are then unspecified (nothing outside the given
+ *     tensors is touched).
  *
  * Short causal depthwise convolution with bias and SiLU, ahead of the delta rule's q, k, v
  * or the scan's x, b, c (all side by side as the D channels):
@@ -412,8 +417,6 @@ size_t kda_noalloc_scratch_bytes(void);
  * be initial_state. A decode step is the dense mode with T = 1.
  *   W           2, 3 or 4.   D: any.   weight [D, W], bias [D] or NULL: w_dtype.
  * Rows that are whole 16-byte pieces at 16-byte aligned addresses move fastest; others work.
- * In packed mode tiles are found by searching the offsets, so where some slot's offsets are
- * broken other slots' rows may be left unwritten too.
  */
 enum kda_activation {
     KDA_ACT_NONE = 0,

@@ -226,6 +226,12 @@ def test_row_strides():
     assert f("x", wide[:1], 2) == 40
     assert f("x", torch.zeros(2, 0, 40), 2) == 40
     assert f("x", wide.view(2, 6, 4, 10), 2) == 40
+    line = torch.zeros(8)
+    assert f("x", line, 0) == 8
+    with pytest.raises(ValueError):
+        f("x", line[::2], 0)                             # one row whose elements are apart
+    with pytest.raises(ValueError):
+        f("x", torch.zeros(4)[::2], 0)
     with pytest.raises(ValueError):
         f("x", wide[:, 1:], 2)
     with pytest.raises(ValueError):

@@ -170,6 +170,16 @@ def test_conv_in_place_state_of_packed_prompts():
     assert torch.equal(y, y2) and torch.equal(final, s)
 
 
+def test_outputs_that_are_inputs_are_refused():
+    c = conv_case(9, BF, BF, 4, 64, B=2, T=9)
+    with pytest.raises(ValueError):
+        kda.kda_conv_fwd(**c, out=c["x"])
+    s = ssm_case(9, H=1, HV=2, T=9)
+    for f in (kda.kda_ssm_chunk_fwd, kda.kda_ssm_recurrent_fwd):
+        with pytest.raises(ValueError):
+            f(**s, out=s["x"])
+
+
 def test_conv_packed_is_the_dense_runs():
     lens = [5, 33, 0, 64]
     c = conv_case(3, BF, BF, 4, 96, lens=lens)
@@ -378,6 +388,35 @@ def test_scan_many_sequences_and_long_packed():
         ssm_check(c, kda.kda_ssm_chunk_fwd, True)
 
 
+def test_two_scans_at_once():
+    """Calls on two streams with nothing shared, again and again, are the calls by themselves."""
+    cases = [ssm_case(60, H=1, HV=4, K=128, V=64, T=3000), ssm_case(61, H=2, HV=4, lens=[700, 0, 1300, 64], K=128, V=128)]
+    alone = [kda.kda_ssm_chunk_fwd(**c, output_final_state=True) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(4):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(kda.kda_ssm_chunk_fwd(**c, output_final_state=True))
+    torch.cuda.synchronize()
+    for i, (y, f) in enumerate(got):
+        assert torch.equal(y, alone[i % 2][0]) and torch.equal(f, alone[i % 2][1])
+
+
+def test_scan_workspace_of_the_callers():
+    """A workspace given by the caller, dirty from another problem, changes nothing."""
+    c = ssm_case(62, H=1, HV=2, K=64, V=64, T=2000)
+    y, f = kda.kda_ssm_chunk_fwd(**c, output_final_state=True)
+    need = kda.kda_ssm_chunk_fwd_workspace_bytes(1, 2000, 1, 2, 64, 64, 1, False, BF)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        y2, f2 = kda.kda_ssm_chunk_fwd(**c, output_final_state=True, workspace=ws)
+        assert torch.equal(y, y2) and torch.equal(f, f2)
+    with pytest.raises(kda.KdaError):
+        kda.kda_ssm_chunk_fwd(**c, workspace=ws[:need - 256])
+
+
 # ------------------------------------------------------------------------------ the norm
 NORM = [(1, 1), (3, 3), (5, 64), (7, 96), (4, 128), (9, 200), (2, 256), (3, 500), (6, 512), (5, 1000), (3, 1024), (5, 2048),
         (3, 2056), (2, 4096), (1030, 4096), (2, 5120), (2, 8192), (2, 8191), (1, 20480), (1, 32768), (0, 64), (1100, 40)]
@@ -490,6 +529,8 @@ def test_norm_strides_aliases_and_odd_values():
     assert torch.allclose(kda.kda_rmsnorm_fwd(odd, w)[0].float(), kda.kda_rmsnorm_fwd(odd.contiguous(), w)[0].float(), rtol=2.0 ** -7)
     with pytest.raises(kda.KdaError):
         kda.kda_rmsnorm_quant_fwd(odd, w, group=128)
+    one = randn(g, 96, dtype=BF)     # a single row, without an axis for it
+    assert torch.equal(kda.kda_rmsnorm_fwd(one, w[:96])[0], kda.kda_rmsnorm_fwd(one[None], w[:96])[0][0])
     # h into the residual, y into x
     a, res = x.contiguous(), randn(g, 2, 9, 256, dtype=BF)
     y, h, _ = kda.kda_rmsnorm_fwd(a, w, res)
