@@ -5,7 +5,8 @@
 // -- the delta rule's recurrence with one decay per head and no erase. The state's layout,
 // the work decomposition (one wave per sequence, head and BV-column slice, its state in
 // registers) and the rule for BV are those of the delta rule's kernel: a step of one token
-// is a pure stream of states, 2 x 4 K V bytes a head against 4 K V flops.
+// is a pure stream of states, 2 x 4 K V bytes a head against 4 K V flops: 1024 sequences x 32
+// heads, K = V = 128, 0.73 ms (5.9 TB/s).
 #include "kda_layer.h"
 #include "kda_state_rows.h"
 
