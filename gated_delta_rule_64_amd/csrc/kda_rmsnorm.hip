@@ -252,23 +252,29 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd_kernel(cons
     }
 }
 
-// threads of a row and accesses of a thread for `n` accesses a row
+// Threads of a row and accesses of a thread for `n` accesses a row. Up to 128 both directions
+// stay inside a wave. Beyond, the forward does best with four accesses a thread before it
+// takes more threads (8192 x 2048 bf16: one wave of four 19 us, four waves of one 21; 4096 x
+// 8192: four waves of four 36 us, sixteen of one 40; 8192 x 4096: one wave of eight 40 us, four
+// of two 38), the backward, which holds three rows and the weight's sums, with as few as it
+// can (the same sizes: 33 and 25 us, 59 and 44, 89 and 41).
 struct Shape { int tpr, nv; };
-inline Shape shape_of(int n, int vec) {
+inline Shape shape_of(int n, int vec, bool bwd) {
     if (vec == 4 && n <= 32) return {32, 1};   // 128 fp32 columns are 32 lanes
     if (n <= 16) return {16, 1};
     if (n <= 32) return {16, 2};
     if (n <= 64) return {32, 2};
     if (n <= 128) return {64, 2};
-    if (n <= 256) return {64, 4};
+    if (n <= 256) return bwd ? Shape{256, 1} : Shape{64, 4};
     if (n <= 512) return {256, 2};
-    if (n <= 1024) return {256, 4};
+    if (n <= 1024) return bwd ? Shape{1024, 1} : Shape{256, 4};
+    if (n <= 2048 && bwd) return {1024, 2};
     if (n <= 4096) return {1024, 4};
     return {1024, 8};
 }
 
 // `go` is a struct with a call operator template <TPR, NV>
-template <int VEC, typename F> hipError_t by_shape(const Shape& s, const F& go) {
+template <int VEC, bool BWD, typename F> hipError_t by_shape(const Shape& s, const F& go) {
     if (s.tpr == 16) {
         if constexpr (VEC != 4) return s.nv == 1 ? go.template operator()<16, 1>() : go.template operator()<16, 2>();
     }
@@ -276,8 +282,15 @@ template <int VEC, typename F> hipError_t by_shape(const Shape& s, const F& go) 
         if constexpr (VEC == 4) { if (s.nv == 1) return go.template operator()<32, 1>(); }
         return go.template operator()<32, 2>();
     }
-    if (s.tpr == 64) return s.nv == 2 ? go.template operator()<64, 2>() : go.template operator()<64, 4>();
-    if (s.tpr == 256) return s.nv == 2 ? go.template operator()<256, 2>() : go.template operator()<256, 4>();
+    if constexpr (BWD) {
+        if (s.tpr == 64) return go.template operator()<64, 2>();
+        if (s.tpr == 256) return s.nv == 1 ? go.template operator()<256, 1>() : go.template operator()<256, 2>();
+        if (s.nv == 1) return go.template operator()<1024, 1>();
+        if (s.nv == 2) return go.template operator()<1024, 2>();
+    } else {
+        if (s.tpr == 64) return s.nv == 2 ? go.template operator()<64, 2>() : go.template operator()<64, 4>();
+        if (s.tpr == 256) return s.nv == 2 ? go.template operator()<256, 2>() : go.template operator()<256, 4>();
+    }
     return s.nv == 4 ? go.template operator()<1024, 4>() : go.template operator()<1024, 8>();
 }
 
@@ -296,7 +309,7 @@ template <typename T, int VEC> struct Fwd {
     template <int TPR, int NV> hipError_t operator()() const { return fwd_n<T, VEC, TPR, NV>(a); }
 };
 template <typename T, int VEC> hipError_t fwd_v(const NormArgs& a) {
-    return by_shape<VEC>(shape_of((a.D + VEC - 1) / VEC, VEC), Fwd<T, VEC>{a});
+    return by_shape<VEC, false>(shape_of((a.D + VEC - 1) / VEC, VEC, false), Fwd<T, VEC>{a});
 }
 
 inline int bwd_rows_per_block(const Shape& s) { return s.tpr < 256 ? 256 / s.tpr : 1; }
@@ -320,9 +333,9 @@ template <typename T, int VEC> struct Bwd {
     template <int TPR, int NV> hipError_t operator()() const { return bwd_n<T, VEC, TPR, NV>(a, blocks); }
 };
 template <typename T, int VEC> hipError_t bwd_v(const NormBwdArgs& a) {
-    const Shape s = shape_of((a.D + VEC - 1) / VEC, VEC);
+    const Shape s = shape_of((a.D + VEC - 1) / VEC, VEC, true);
     const int blocks = bwd_blocks(a.rows, s);
-    const hipError_t err = by_shape<VEC>(s, Bwd<T, VEC>{a, blocks});
+    const hipError_t err = by_shape<VEC, true>(s, Bwd<T, VEC>{a, blocks});
     if (err != hipSuccess) return err;
     SumRows r;
     r.part = a.partial; r.P = blocks; r.M = a.D; r.out = a.dweight; r.out_tail = nullptr; r.D = a.D; r.taps = 1;
@@ -334,7 +347,7 @@ template <typename T, int VEC> hipError_t bwd_v(const NormBwdArgs& a) {
 int norm_bwd_partials(long long rows, int D, int dtype) {
     // the scalar and the 16-byte form differ in their blocks: room for either
     const int vec = dtype == KDA_BF16 ? 8 : 4;
-    const int wide = bwd_blocks(rows, shape_of((D + vec - 1) / vec, vec)), narrow = bwd_blocks(rows, shape_of(D, 1));
+    const int wide = bwd_blocks(rows, shape_of((D + vec - 1) / vec, vec, true)), narrow = bwd_blocks(rows, shape_of(D, 1, true));
     return wide > narrow ? wide : narrow;
 }
 

@@ -828,14 +828,17 @@ __global__ __launch_bounds__(K * SLAB / 4 / JOIN_PARTS) void ssm_join_kernel(con
 
 // Dense sequences are cut only where their blocks would leave half the chip's 256 units idle
 // (N x units <= 128), into pieces of at least SEG_MIN chunks, for about BLOCKS_WANTED blocks,
-// two a unit: 32768 tokens x 64 heads 362 us (256 blocks 407, 768 396, 1024 384). With 129 to
-// 511 blocks the first pass would cost what the second gains.
+// two a unit: 32768 tokens x 64 heads 362 us (256 blocks 407, 768 396, 1024 384). N x 4096
+// tokens x 32 heads, K = V = 128, cut and whole: N x units = 64 105 and 240 us, 128 184 and
+// 263, 192 267 and 270, 256 313 and 279 (the first pass then costs what the second gains).
 constexpr int SEG_MIN = 4;
 constexpr long long BLOCKS_WANTED = 512;
 
 Plan plan_of(int B, int T, int H, int HV, int K, int V, int N, bool packed, int dtype) {
     Plan p;
     p.slabs = HV * (V / SLAB);
+    // two slabs a block share b, c and their products where a group has an even number of slabs
+    // (32768 tokens x 64 heads: 367 us, one slab a block 428)
     p.ns = dtype == KDA_BF16 && (p.slabs / H) % 2 == 0 ? 2 : 1;
     p.units = p.slabs / p.ns;
     const long long chunks = (T + C - 1) / C;
