@@ -83,7 +83,7 @@ def _want(name, t, shape, dtypes, dev=None):
         names = " or ".join(str(d).replace("torch.", "") for d in dtypes)
         raise TypeError(f"{name}: got dtype {str(t.dtype).replace('torch.', '')}, expected {names}")
     if dev is not None:
-        if t.device != dev or not t.is_cuda:
+        if t.device != dev:
             _placed(name, t, dev)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -211,14 +211,14 @@ def kda_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, outp
     lib = _load()
     B, T, D, W, N, code, w_code, stride, dev = _conv_inputs(x, weight, bias, initial_state, cu_seqlens, activation)
     if out is None:
-        out = torch.empty(B, T, D, dtype=x.dtype, device=dev)
+        out = x.new_empty((B, T, D))
     else:
         _want("out", out, (B, T, D), (x.dtype,), dev)
         _apart("out", out, (("x", x), ("initial_state", initial_state)))
     if not output_final_state:
         final_state = None
     elif final_state is None:
-        final_state = torch.empty(N, W - 1, D, dtype=x.dtype, device=dev)
+        final_state = x.new_empty((N, W - 1, D))
     else:
         _want("final_state", final_state, (N, W - 1, D), (x.dtype,), dev)
     dev_status = _status(dev, dev_status, cu_seqlens, debug)
@@ -281,14 +281,14 @@ def _ssm(chunk, x, dt, A_log, b, c, D, dt_bias, initial_state, cu_seqlens, outpu
     _want("dt_bias", dt_bias, (HV,), _F32, dev)
     _want("initial_state", initial_state, (N, HV, K, V), _F32, dev)
     if out is None:
-        out = torch.empty(B, T, HV, V, dtype=x.dtype, device=dev)
+        out = x.new_empty((B, T, HV, V))
     else:
         _want("out", out, (B, T, HV, V), (x.dtype,), dev)
         _apart("out", out, (("x", x), ("b", b), ("c", c), ("dt", dt)))
     if not output_final_state:
         final_state = None
     elif final_state is None:
-        final_state = torch.empty(N, HV, K, V, dtype=torch.float32, device=dev)
+        final_state = A_log.new_empty((N, HV, K, V))
     else:
         _want("final_state", final_state, (N, HV, K, V), _F32, dev)
     dev_status = _status(dev, dev_status, cu_seqlens, debug)
@@ -360,7 +360,7 @@ def kda_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, output_rstd=False, ou
     lib = _load()
     shape, rows, D, code, w_code, stride, dev = _norm_inputs(x, weight, residual)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(shape)
     else:
         _want("out", out, shape, (x.dtype,), dev)
     h = _sum_buffer(shape, x, residual, residual_out, dev)
@@ -376,7 +376,7 @@ def _sum_buffer(shape, x, residual, residual_out, dev):
             raise ValueError("residual_out belongs to a residual")
         return None
     if residual_out is None:
-        return torch.empty(shape, dtype=x.dtype, device=dev)
+        return x.new_empty(shape)
     _want("residual_out", residual_out, shape, (x.dtype,), dev)
     return residual_out
 
@@ -423,7 +423,7 @@ def kda_rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, workspace=None):
     _want("h", h, shape, _FLOAT, dev)
     _want("dy", dy, shape, (h.dtype,), dev)
     _want("rstd", rstd, shape[:-1], _F32, dev)
-    dx = torch.empty(shape, dtype=h.dtype, device=dev)
+    dx = h.new_empty(shape)
     dweight = torch.empty(D, dtype=torch.float32, device=dev)
     workspace = _bytes("workspace", workspace, lib.kda_rmsnorm_bwd_workspace_bytes(rows, D, code), dev)
     _call(dev, lib.kda_rmsnorm_bwd, _at(dy), _at(h), _at(weight), _at(rstd), _at(dh), _at(dx), _at(dweight), rows, D,
