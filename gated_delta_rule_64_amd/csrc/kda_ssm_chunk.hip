@@ -135,7 +135,6 @@ struct alignas(16) Steps {
     float dt[C];
     float hi[C], lo[C];   // running sums of the log2 decay, as hi + lo
     float grow[C];        // 2^(cum_63 - cum_j) dt'_j
-    float fall[C];        // 2^(cum_i)
     float all;            // 2^(cum_63)
 };
 
@@ -265,13 +264,11 @@ __device__ __forceinline__ double place_steps(const Step& v, int cl, Steps* s) {
     const int j = threadIdx.x & 63;
     const float dt = j < cl ? v.dt : 0.f;
     const float eh = __shfl(v.hi, 63, 64), el = __shfl(v.lo, 63, 64);
-    const float fall = exp2_fast(v.hi);
     s->dt[j] = dt;
     s->hi[j] = v.hi;
     s->lo[j] = v.lo;
     s->grow[j] = exp2_fast((eh - v.hi) + (el - v.lo)) * dt;
-    s->fall[j] = fall;
-    if (j == 63) s->all = fall;
+    if (j == 63) s->all = exp2_fast(v.hi);
     return (double)eh + (double)el;
 }
 
@@ -424,7 +421,7 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
 #pragma unroll
                     for (int r = 0; r < 4; ++r) acc = Mma<float>::mma(S[t][r], v[r], acc);
                 }
-                const float f = st.fall[i];
+                const float f = exp2_fast(st.hi[i]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[r] *= f;
 #pragma unroll
@@ -472,21 +469,25 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
 // bf16 inputs: the bf16 matrix cores, NS slabs of one b / c group a block. Two slabs: a wave
 // holds 32 columns of one of them (two column tiles), so that what it reads of b and c, the
 // most of its LDS traffic, serves twice; one slab: 16 columns.
-//   * c_i . b_j is exact bf16 products summed in fp32; M is rounded to bf16 once after its
-//     weights, and the state once as the operand of S^T c: half a bf16 step of every term,
-//     which is what y's own storage costs.
+//   * c_i . b_j is exact bf16 products summed in fp32; M after its weights, and the state as
+//     the operand of S^T c, are pairs of bf16 (a value rounded and the rest of it rounded: 2^-16
+//     of every term), so that y is rounded once, where it is stored: its error against 64 bits is
+//     that rounding's 1.7e-3, where one bf16 for each left up to 2.1e-3 (a packed batch of 64
+//     prompts, in 161 us instead of 175; 8192 tokens x 32 heads 115 and 123).
 //   * the state is kept to fp32: each weighted x is cut into three bf16 (24 bits), so its
 //     update is three products.
 //   * operands whose contraction runs over tokens (x and b down a column) are read from LDS
 //     transposed (ds_read_b64_tr_b16: four consecutive rows of a column a lane).
 //   * rows past the sequence's end are loaded as zeros and their stores dropped by the bounds
 //     of the buffer descriptors (made for every chunk), without branches.
-// Rows in LDS are 32 bytes longer than their data, and every eight rows begin 16 bytes
-// later: the transposed reads' half waves (8 rows x 32 bytes) and the row-wise 8-byte operand
-// reads' (16 rows x 16 bytes) then both meet every bank once.
+// Rows of b and x in LDS are 32 bytes longer than their data, and every eight rows begin 16
+// bytes later: the transposed reads' half waves (8 rows x 32 bytes) and the row-wise 8-byte
+// operand reads' (16 rows x 16 bytes) then both meet every bank once. c is read by rows only:
+// 16 bytes of gap a row do for it.
 // ---------------------------------------------------------------------------------
 constexpr int GAP = 16;   // elements
 template <int LD> __device__ __forceinline__ constexpr int row_at(int r) { return r * LD + 8 * (r >> 3); }
+constexpr int GAP_C = 8;
 
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
@@ -525,8 +526,16 @@ __device__ __forceinline__ void split3(bf16x8 x, int e, float w0, float w1, bf16
 }
 __device__ __forceinline__ f32x4 mma32(bf16x8 a, bf16x8 b, f32x4 c) { return Mma<__bf16>::mma(a, b, c); }
 
-// where M's operand fragment of token block I, step s (token blocks 2s and 2s+1) is kept
-__device__ __forceinline__ constexpr int m_frag(int I, int s) { return I < 2 ? I : 2 * I - 2 + s; }
+// where M's tile of token blocks I and J <= I is kept: a lane's four values in accumulator
+// order as bf16, and then what their rounding left
+__device__ __forceinline__ constexpr int m_tile(int I, int J) { return I * (I + 1) / 2 + J; }
+// v as hi + lo
+__device__ __forceinline__ void split2(f32x4 v, bf16x4& hi, bf16x4& lo) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) hi[r] = (__bf16)v[r];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) lo[r] = (__bf16)(v[r] - (float)hi[r]);
+}
 
 // a descriptor of `bytes` bytes at p: loads past them give 0, stores there are dropped
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, unsigned bytes) {
@@ -541,11 +550,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
     constexpr int KT = K / 16, KS = K / 32;
     constexpr int THREADS = 64 * WAVES;
     constexpr int CT = 4 * NS / WAVES;                                          // column tiles of a wave
-    constexpr int LDK = K + GAP, LDX = SLAB + GAP;
+    constexpr int LDK = K + GAP, LDC = K + GAP_C, LDX = SLAB + GAP;
     constexpr int NB = C * K / 8 / THREADS, NX = C * SLAB / 8 / THREADS;   // 16-byte pieces a thread
     constexpr int RB = THREADS / (K / 8), RX = THREADS / (SLAB / 8);       // rows between them
-    __shared__ __attribute__((aligned(16))) __bf16 Bs[row_at<LDK>(C)], Cs[FIRST ? 8 : row_at<LDK>(C)], Xs[NS][row_at<LDX>(C)];
-    __shared__ __attribute__((aligned(16))) __bf16 Ms[FIRST ? 1 : NS][FIRST ? 8 : 6 * 64 * 8];
+    __shared__ __attribute__((aligned(16))) __bf16 Bs[row_at<LDK>(C)], Cs[FIRST ? 8 : LDC * C], Xs[NS][row_at<LDX>(C)];
+    __shared__ __attribute__((aligned(16))) __bf16 Ms[FIRST ? 1 : NS][FIRST ? 8 : 10 * 64 * 8];
     __shared__ Steps steps[2][NS];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int l16 = lane & 15, g = lane >> 4;
@@ -578,9 +587,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
     const __bf16* xp = static_cast<const __bf16*>(a.x) + w.row0 * a.x_stride + (size_t)slab0 * SLAB;
     const unsigned bs2 = (unsigned)a.b_stride * 2, cs2 = (unsigned)a.c_stride * 2, xs2 = (unsigned)a.x_stride * 2;
     const unsigned b_at = tb * bs2 + kb * 2, c_at = tb * cs2 + kb * 2, x_at = tx * xs2 + kx * 2;
-    const int putk = row_at<LDK>(tb) + kb, putx = row_at<LDX>(tx) + kx;
-    // this lane's place in a row-wise operand, in a transposed one of b, and of x
-    const int rowk = row_at<LDK>(l16) + 4 * g;
+    const int putk = row_at<LDK>(tb) + kb, putc = LDC * tb + kb, putx = row_at<LDX>(tx) + kx;
+    // this lane's place in a row-wise operand of b and of c, in a transposed one of b, and of x
+    const int rowk = row_at<LDK>(l16) + 4 * g, rowc = LDC * l16 + 4 * g;
     const int colb = row_at<LDK>(lane >> 2) + 4 * (lane & 3);
     const int colx = row_at<LDX>(lane >> 2) + base + 4 * NS * (lane & 3);
     bf16x8 rb[NB], rc[FIRST ? 1 : NB], rx[NS][NX];
@@ -623,15 +632,6 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
 #pragma unroll
         for (int u = 0; u < CT; ++u) store_slot(S[u], p.starts, p, w.slot0, slab, part(u));
     const float skip = a.D ? a.D[slab / vs] : 0.f;
-    if constexpr (!FIRST) {
-        // the halves of M's fragments above the diagonal: token blocks 1 of I = 0, 3 of I = 2
-        if (wave == 0)
-#pragma unroll
-            for (int v = 0; v < NS; ++v) {
-                *reinterpret_cast<bf16x4*>(Ms[v] + (m_frag(0, 0) * 64 + lane) * 8 + 4) = bf16x4{};
-                *reinterpret_cast<bf16x4*>(Ms[v] + (m_frag(2, 1) * 64 + lane) * 8 + 4) = bf16x4{};
-            }
-    }
     if (begin < stop) {
         form_steps(begin);
         if (begin + C < stop) fetch_steps(begin + C);
@@ -646,7 +646,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             *reinterpret_cast<bf16x8*>(Bs + putk + row_at<LDK>(i * RB)) = rb[i];
-            if constexpr (!FIRST) *reinterpret_cast<bf16x8*>(Cs + putk + row_at<LDK>(i * RB)) = rc[i];
+            if constexpr (!FIRST) *reinterpret_cast<bf16x8*>(Cs + putc + LDC * i * RB) = rc[i];
         }
 #pragma unroll
         for (int i = 0; i < NX; ++i)
@@ -678,46 +678,51 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
                 f32x4 cb = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
-                    cb = mma32(read_row(Bs + rowk + row_at<LDK>(16) * J, s), read_row(Cs + rowk + row_at<LDK>(16) * I, s), cb);
+                    cb = mma32(read_row(Bs + rowk + row_at<LDK>(16) * J, s), read_row(Cs + rowc + LDC * 16 * I, s), cb);
 #pragma unroll
                 for (int v = 0; v < NS; ++v) {
                     const f32x4 hj = *reinterpret_cast<const f32x4*>(st[v].hi + j0), lj = *reinterpret_cast<const f32x4*>(st[v].lo + j0);
                     const f32x4 dj = *reinterpret_cast<const f32x4*>(st[v].dt + j0);
                     const float hi = st[v].hi[i], lo = st[v].lo[i];
-                    bf16x4 m;
+                    f32x4 m;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float e = exp2_fast((hi - hj[r]) + (lo - lj[r])) * dj[r];
-                        m[r] = (__bf16)(j0 + r <= i ? cb[r] * e : 0.f);
+                        m[r] = j0 + r <= i ? cb[r] * e : 0.f;
                     }
-                    *reinterpret_cast<bf16x4*>(Ms[v] + (m_frag(I, J >> 1) * 64 + lane) * 8 + 4 * (J & 1)) = m;
+                    bf16x4 mh, ml;
+                    split2(m, mh, ml);
+                    *reinterpret_cast<bf16x8*>(Ms[v] + (m_tile(I, J) * 64 + lane) * 8) = join(mh, ml);
                 }
             }
             // S^T c of the chunk's four token blocks, scaled by the tokens' decays
-            bf16x8 sf[CT][KS];
 #pragma unroll
-            for (int u = 0; u < CT; ++u)
-#pragma unroll
-                for (int s = 0; s < KS; ++s)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        sf[u][s][r] = (__bf16)S[u][2 * s][r];
-                        sf[u][s][4 + r] = (__bf16)S[u][2 * s + 1][r];
-                    }
-#pragma unroll
-            for (int I = 0; I < 4; ++I) {
+            for (int I = 0; I < 4; ++I)
 #pragma unroll
                 for (int u = 0; u < CT; ++u) acc[u][I] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const bf16x8 cf = read_row(Cs + rowk + row_at<LDK>(16 * I), s);
+            for (int s = 0; s < KS; ++s) {
+                bf16x8 sh[CT], sl[CT];
 #pragma unroll
-                    for (int u = 0; u < CT; ++u) acc[u][I] = mma32(sf[u][s], cf, acc[u][I]);
+                for (int u = 0; u < CT; ++u) {
+                    bf16x4 h0, l0, h1, l1;
+                    split2(S[u][2 * s], h0, l0);
+                    split2(S[u][2 * s + 1], h1, l1);
+                    sh[u] = join(h0, h1);
+                    sl[u] = join(l0, l1);
+                }
+#pragma unroll
+                for (int I = 0; I < 4; ++I) {
+                    const bf16x8 cf = read_row(Cs + rowc + LDC * 16 * I, s);
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) acc[u][I] = mma32(sl[u], cf, acc[u][I]);
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) acc[u][I] = mma32(sh[u], cf, acc[u][I]);
                 }
             }
 #pragma unroll
             for (int I = 0; I < 4; ++I) {
-                const float f = st[q].fall[16 * I + l16];
+                const float f = exp2_fast(st[q].hi[16 * I + l16]);
 #pragma unroll
                 for (int u = 0; u < CT; ++u)
 #pragma unroll
@@ -729,9 +734,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
             for (int I = 0; I < 4; ++I) {
 #pragma unroll
                 for (int s = 0; s <= (I >> 1); ++s) {
-                    const bf16x8 m = *reinterpret_cast<const bf16x8*>(Ms[q] + (m_frag(I, s) * 64 + lane) * 8);
+                    // token blocks 2 s and 2 s + 1, the second above the diagonal where I = 2 s
+                    const bf16x8 m0 = *reinterpret_cast<const bf16x8*>(Ms[q] + (m_tile(I, 2 * s) * 64 + lane) * 8);
+                    bf16x8 m1{};
+                    if (2 * s + 1 <= I) m1 = *reinterpret_cast<const bf16x8*>(Ms[q] + (m_tile(I, 2 * s + 1) * 64 + lane) * 8);
+                    const bf16x8 mh = __builtin_shufflevector(m0, m1, 0, 1, 2, 3, 8, 9, 10, 11);
+                    const bf16x8 ml = __builtin_shufflevector(m0, m1, 4, 5, 6, 7, 12, 13, 14, 15);
 #pragma unroll
-                    for (int u = 0; u < CT; ++u) acc[u][I] = mma32(xf[u][s], m, acc[u][I]);
+                    for (int u = 0; u < CT; ++u) acc[u][I] = mma32(xf[u][s], ml, acc[u][I]);
+#pragma unroll
+                    for (int u = 0; u < CT; ++u) acc[u][I] = mma32(xf[u][s], mh, acc[u][I]);
                 }
                 // columns base + 4 NS g .. of token 16 I + l % 16
                 const __bf16* xi = Xs[q] + row_at<LDX>(l16) + base + 4 * CT * g + row_at<LDX>(16 * I);

@@ -1,0 +1,52 @@
+"""Parity of the operators around the mixer where their precision, odd values and sizes are
+at stake. Bounds as in test_layer_gpu: EPS is fp32's half step, OUT a stored type's."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_64_amd as kda
+from oracle import layer
+from tests.test_layer_gpu import BF, DEV, EPS, F32, OUT, conv_case, f64, gen, near, offsets, randn, ssm_case
+
+pytestmark = pytest.mark.gpu
+
+SCANS = [kda.kda_ssm_chunk_fwd, kda.kda_ssm_recurrent_fwd]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _ready():
+    kda.load_library()
+    assert torch.cuda.is_available()
+    yield
+
+
+def scan_oracle(c):
+    B, T, HV, V = c["x"].shape
+    H, K = c["b"].shape[2:]
+    r = lambda t, *s: f64(t).reshape(B * T, *s)  # noqa: E731
+    seqs = layer.spans(B, T, None if c["cu_seqlens"] is None else c["cu_seqlens"].tolist())
+    return layer.ssm(r(c["x"], HV, V), r(c["dt"], HV), f64(c["A_log"]), r(c["b"], H, K), r(c["c"], H, K), f64(c["D"]),
+                     f64(c["dt_bias"]), f64(c["initial_state"]), seqs, c["dt_softplus"])
+
+
+# ------------------------------------------------------------------------------ the scan
+@pytest.mark.parametrize("H,HV,K,V", [(1, 2, 64, 64), (1, 1, 128, 128), (2, 2, 128, 64), (1, 3, 128, 128), (1, 4, 128, 64)])
+def test_scan_operands_keep_16_bits(H, HV, K, V):
+    """A first token's product read by every later one, in its chunk (M) and from the state, and
+    the read-out's leading bits taken away by the skip: what is left shows the operands' own
+    roundings. dt' is 0 after the first token, so nothing decays and nothing else is written."""
+    T = 150
+    c = ssm_case(1, BF, H, HV, K, V, T=T, state=False, softplus=False, bias=False, dt_dtype=F32, a_log=0.0)
+    g = gen(2)
+    c["dt"][:, 1:] = 0
+    c["dt"][:, 0] = torch.rand(HV, generator=g, device=DEV) + 0.5
+    c["b"][:, 0] = 0
+    c["b"][:, 0, :, 5] = 1.375
+    c["D"] = torch.full((HV,), -1.0, device=DEV)
+    # c . b dt' x is one product, and its leading bits are x of the later tokens
+    m = c["c"][..., 5].double().repeat_interleave(HV // H, 2) * 1.375 * c["dt"][:, :1].double()
+    c["x"][:, 1:] = (m[..., None] * c["x"][:, :1].double()).to(BF)[:, 1:]
+    y, _ = kda.kda_ssm_chunk_fwd(**c)
+    wy, _, my, _ = scan_oracle(c)
+    # a pair of bf16 is off by at most 2^-8 of 2^-8; M, the state and the sums by fp32 steps
+    near("y", y.view(T, HV, V), wy, (2.0 ** -16 * 1.01 + 16 * EPS) * my + OUT[BF] * 1.01 * np.abs(wy))
