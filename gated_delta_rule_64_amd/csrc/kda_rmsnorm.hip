@@ -73,6 +73,19 @@ template <int VEC> __device__ __forceinline__ void store_fp8(uint8_t* p, const f
     }
 }
 
+// v / s rounded once, for many v and one s: v times the rounded 1 / s, and one step of its
+// remainder (v - q s, exact in an fma) back onto it. A value near a tie of two codes takes the
+// neighbour's if the product alone stands for the quotient. An infinite s gives 0 (the remainder's
+// factor is taken as 0), as the division does.
+struct Divisor {
+    float inv, back;
+    __device__ __forceinline__ explicit Divisor(float s) : inv(1.f / s), back(s < __builtin_inff() ? -s : 0.f) {}
+    __device__ __forceinline__ float quotient(float v) const {
+        const float q = v * inv;
+        return fmaf(fmaf(back, q, v), inv, q);
+    }
+};
+
 template <typename T, int VEC, int TPR, int NV, bool QUANT>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(const NormArgs a) {
     constexpr int THREADS = TPR < 256 ? 256 : TPR;
@@ -122,7 +135,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(cons
         float w[VEC];
         load_param<VEC>(a.weight, a.w_dtype, d, w);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) h[i][e] *= rstd * w[e];
+        for (int e = 0; e < VEC; ++e) h[i][e] = h[i][e] * rstd * w[e];
         if constexpr (!QUANT) {
             store_vec<VEC>(static_cast<T*>(a.y) + at + d, h[i]);
         } else {
@@ -136,13 +149,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(cons
             top = row_reduce<TPR, true>(top, slot, 1);
             const float s = fmaxf(top, FP8_TINY) / FP8_MAX;
             if (tid == 0) a.scales[row] = s;
-            const float inv = 1.f / s;
+            const Divisor by(s);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int d = (i * TPR + tid) * VEC;
                 if (d >= a.D) continue;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) h[i][e] *= inv;
+                for (int e = 0; e < VEC; ++e) h[i][e] = by.quotient(h[i][e]);
                 store_fp8<VEC>(q + d, h[i]);
             }
         } else if constexpr (VEC > 1 && TPR * VEC >= 128) {
@@ -159,9 +172,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(cons
                 if (d >= a.D) continue;
                 const float s = fmaxf(m, FP8_TINY) / FP8_MAX;
                 if ((tid & (GL - 1)) == 0) a.scales[row * per_row + d / 128] = s;
-                const float inv = 1.f / s;
+                const Divisor by(s);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) h[i][e] *= inv;
+                for (int e = 0; e < VEC; ++e) h[i][e] = by.quotient(h[i][e]);
                 store_fp8<VEC>(q + d, h[i]);
             }
         }

@@ -50,3 +50,31 @@ def test_scan_operands_keep_16_bits(H, HV, K, V):
     wy, _, my, _ = scan_oracle(c)
     # a pair of bf16 is off by at most 2^-8 of 2^-8; M, the state and the sums by fp32 steps
     near("y", y.view(T, HV, V), wy, (2.0 ** -16 * 1.01 + 16 * EPS) * my + OUT[BF] * 1.01 * np.abs(wy))
+
+
+# ------------------------------------------------------------------------------ the norm
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_codes_are_those_of_the_quotient(group, dtype):
+    """Rows of +-1 and eps 0 have r = 1 exactly, so y is the weight: the codes are e4m3 of the fp32
+    quotient y / s, here for weights at and beside every tie between codes."""
+    D, rows = 1024, 3
+    codes = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    ties = (codes[:-1] + codes[1:]) / 2
+    rng = np.random.default_rng(50)
+    w = torch.empty(D)
+    for at in range(0, D, 128):
+        top = np.float32(rng.uniform(0.5, 2.0))
+        s = np.float32(top / np.float32(448))
+        v = (ties[torch.tensor(rng.permutation(126)[:127])].numpy() * s).astype(np.float32)
+        v = v.view(np.int32) + rng.integers(-2, 3, v.size).astype(np.int32)
+        w[at:at + 128] = torch.tensor(np.concatenate([[top, -top], v.view(np.float32)]).astype(np.float32))
+    if not group:
+        w[128:] = w[:128].repeat(D // 128 - 1)
+    sign = torch.where(torch.rand(rows, D, generator=torch.Generator().manual_seed(1)) < 0.5, -1.0, 1.0)
+    q, s, _ = kda.kda_rmsnorm_quant_fwd(sign.to(DEV, dtype), w.to(DEV), eps=0.0, group=group)
+    y = sign * w
+    ws = y.view(rows, -1, group or D).abs().amax(-1) / 448.0
+    assert torch.equal(s.cpu().view(ws.shape), ws)
+    want = (y.view(rows, -1, group or D) / ws[..., None]).to(torch.float8_e4m3fn).view(rows, D)
+    assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
