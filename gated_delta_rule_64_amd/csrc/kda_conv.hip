@@ -168,21 +168,25 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
     for (long long tile = p * groups + grp; live && tile < tiles; tile += P * groups) {
         const SeqTile s = seq_tile(tile, a.cu_seqlens, a.N, a.T, TT_BWD, tiles_dense);
         if (s.len < 0) continue;
-        const int end = s.len - s.pos < TT_BWD ? s.len : s.pos + TT_BWD;   // own rows: s.pos .. end-1
-        const int first = s.pos == 0 ? -(W - 1) : s.pos;                   // rows whose gradient is written
-        const T* xp = static_cast<const T*>(a.x) + s.row0 * a.x_stride + d;
-        const T* yp = static_cast<const T*>(b.dy) + s.row0 * (long long)a.D + d;
+        // rows counted from the tile's first (a sequence may be 2^31 - 1 rows long): its own
+        // are 0 .. end - 1, the sequence has `rest` of them
+        const int rest = s.len - s.pos;
+        const int end = min(rest, TT_BWD);
+        const int first = s.pos == 0 ? -(W - 1) : 0;   // rows whose gradient is written
+        const T* xp = static_cast<const T*>(a.x) + (s.row0 + s.pos) * a.x_stride + d;
+        const T* yp = static_cast<const T*>(b.dy) + (s.row0 + s.pos) * (long long)a.D + d;
+        T* dxp = static_cast<T*>(b.dx) + (s.row0 + s.pos) * (long long)a.D + d;
         // past the sequence the last row stands in, its dpre taken as 0
         typename Raw<T, VEC>::type cx[RB], cy[RB], nx[RB], ny[RB];
         auto fetch = [&](int t0) {
 #pragma unroll
             for (int k = 0; k < RB; ++k) {
-                const long long t = min(t0 + k, s.len - 1);
+                const long long t = min(t0 + k, rest - 1);
                 nx[k] = load_raw<T, VEC>(xp + t * a.x_stride);
                 ny[k] = load_raw<T, VEC>(yp + t * a.D);
             }
         };
-        if (s.len > 0) fetch(s.pos);
+        if (rest > 0) fetch(0);
         float win[W - 1 + RB][VEC], dp[W - 1 + RB][VEC];   // x and dpre, the last rows and these
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) load_row<T, VEC, W>(a, s, s.pos - (W - 1) + i, d, win[i]);
@@ -190,8 +194,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
         for (int i = 0; i < W - 1; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) dp[i][e] = 0.f;
-        for (int t0 = s.pos; t0 < end + W - 1; t0 += RB) {
-            if (s.len > 0) {
+        for (int t0 = 0; t0 < end + W - 1; t0 += RB) {
+            if (rest > 0) {
 #pragma unroll
                 for (int k = 0; k < RB; ++k) {
                     cx[k] = nx[k];
@@ -202,7 +206,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
 #pragma unroll
             for (int k = 0; k < RB; ++k) {
                 const int t = t0 + k;
-                if (s.len > 0) {
+                if (rest > 0) {
                     widen<T, VEC>(cx[k], win[W - 1 + k]);
                     widen<T, VEC>(cy[k], dp[W - 1 + k]);
                 }
@@ -216,7 +220,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
                         const float sg = sigmoid_fast(acc);
                         g *= sg * (1.f + acc * (1.f - sg));
                     }
-                    g = t < s.len ? g : 0.f;
+                    g = t < rest ? g : 0.f;
                     dp[W - 1 + k][e] = g;
                     if (t < end) {
                         db[e] += g;
@@ -234,7 +238,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
 #pragma unroll
                         for (int i = 0; i < W; ++i) g[e] = fmaf(w[W - 1 - i][e], dp[k + i][e], g[e]);
                     }
-                    const int j = r - (s.len - (W - 1));   // the row of the final state it is handed on as
+                    const int j = r - (rest - (W - 1));   // the row of the final state it is handed on as
                     if (b.dfinal && j >= 0) {
                         float f[VEC];
                         load_vec<VEC>(static_cast<const T*>(b.dfinal) + ((long long)s.n * (W - 1) + j) * a.D + d, f);
@@ -242,7 +246,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
                         for (int e = 0; e < VEC; ++e) g[e] += f[e];
                     }
                     if (r >= 0)
-                        store_vec<VEC>(static_cast<T*>(b.dx) + (s.row0 + r) * (long long)a.D + d, g);
+                        store_vec<VEC>(dxp + r * (long long)a.D, g);
                     else if (b.dinitial)
                         store_vec<VEC>(static_cast<T*>(b.dinitial) + ((long long)s.n * (W - 1) + W - 1 + r) * a.D + d, g);
                 }
@@ -295,11 +299,12 @@ __global__ __launch_bounds__(1024) void sum_rows_kernel(const SumRows s) {
     else if (s.out_tail) s.out_tail[d] = acc;
 }
 
+// tiles of a dense sequence, one at least
+inline int tiles_dense_of(int T, int TT) { return T > 0 ? (T - 1) / TT + 1 : 1; }
 inline long long tiles_of(int B, int T, int N, bool packed, int TT) {
     if (N == 0) return 0;
-    return packed ? (long long)T / TT + N : (long long)B * ((T + TT - 1) / TT > 0 ? (T + TT - 1) / TT : 1);
+    return packed ? (long long)T / TT + N : (long long)B * tiles_dense_of(T, TT);
 }
-inline int tiles_dense_of(int T, int TT) { return (T + TT - 1) / TT > 0 ? (T + TT - 1) / TT : 1; }
 
 // blocks along the rows of the backward, one row of partial sums each: up to 128, then even
 // rounds of them

@@ -52,6 +52,31 @@ def test_scan_operands_keep_16_bits(H, HV, K, V):
     near("y", y.view(T, HV, V), wy, (2.0 ** -16 * 1.01 + 16 * EPS) * my + OUT[BF] * 1.01 * np.abs(wy))
 
 
+# ------------------------------------------------------------------------ the convolution
+def test_conv_longest_sequence():
+    """The longest sequence there can be, one channel wide: its last rows against the
+    convolution of those rows alone."""
+    T, W = 2 ** 31 - 1, 4
+    x = torch.zeros(1, T, 1, dtype=BF, device=DEV)
+    tail = randn(gen(9), 1, 1000, 1, dtype=BF)
+    x[:, -1000:] = tail
+    w, bias = randn(gen(10), 1, W, dtype=BF), randn(gen(11), 1, dtype=BF)
+    y, f = kda.kda_conv_fwd(x, w, bias, output_final_state=True)
+    want, wf = kda.kda_conv_fwd(tail, w, bias, output_final_state=True)
+    assert torch.equal(y[:, -1000:], want) and torch.equal(f, wf)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    assert torch.equal(kda.kda_conv_fwd(x, w, bias, cu_seqlens=cu, debug=True)[0][:, -1000:], want)
+    assert torch.equal(y[:, 5:6].expand(-1, 1000, -1), y[:, T // 2:T // 2 + 1000])
+    del y
+    dy = torch.zeros(1, T, 1, dtype=BF, device=DEV)
+    dy[:, -1000:] = randn(gen(12), 1, 1000, 1, dtype=BF)
+    dx, dw, db, _ = kda.kda_conv_bwd(dy, x, w, bias)
+    wx, ww, wb, _ = kda.kda_conv_bwd(dy[:, -1000:].contiguous(), tail, w, bias)
+    assert torch.equal(dx[:, -1000:], wx) and not dx[:, :1 << 20].any()
+    # the same 1000 terms, added in another order
+    near("dw", dw, f64(ww), 2 * 1004 * EPS * 1.1 * np.abs(f64(dy[:, -1000:])).sum() * np.abs(f64(tail)).max())
+
+
 # ------------------------------------------------------------------------------ the norm
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("group", [0, 128])
