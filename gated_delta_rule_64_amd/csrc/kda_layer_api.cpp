@@ -77,6 +77,10 @@ size_t conv_bwd_need(int B, int T, int D, int W, int N, bool packed) {
     return (size_t)kda::conv_bwd_partials(B, T, D, N, packed) * (size_t)(W + 1) * (size_t)D * sizeof(float);
 }
 
+// positions are counted in int a chunk ahead (rows of 128 bytes and more for each of b and c: no
+// card holds that many)
+constexpr int SSM_MAX_ROWS = 0x7fffffff - 64;
+
 int ssm_args(kda::SsmArgs* a, const void* x, long long x_stride, const void* dt, long long dt_stride,
              const float* A_log, const void* b, long long b_stride, const void* c, long long c_stride, const float* D,
              const float* dt_bias, const float* initial_state, const int32_t* cu_seqlens, int N, void* y,
@@ -86,6 +90,8 @@ int ssm_args(kda::SsmArgs* a, const void* x, long long x_stride, const void* dt,
     if (!is_dtype(dtype) || !is_dtype(dt_dtype))
         return set_error(KDA_ERR_DTYPE, "dtype and dt_dtype must be KDA_BF16 (1) or KDA_F32 (0), got %d and %d", dtype, dt_dtype);
     if (int rc = check_sequences(cu_seqlens, N, B, T)) return rc;
+    if ((long long)B * T > SSM_MAX_ROWS)
+        return set_error(KDA_ERR_SHAPE, "B*T=%lld exceeds %d rows", (long long)B * T, SSM_MAX_ROWS);
     if (H <= 0 || HV <= 0) return set_error(KDA_ERR_SHAPE, "H and HV must be positive: H=%d HV=%d", H, HV);
     if (HV % H != 0) return set_error(KDA_ERR_SHAPE, "HV=%d must be a multiple of H=%d", HV, H);
     if (K != 64 && K != 128) return set_error(KDA_ERR_UNSUPPORTED, "K must be 64 or 128, got %d", K);
@@ -187,7 +193,7 @@ int kda_conv_bwd(const void* dy, const void* x, long long x_stride, const void* 
 
 size_t kda_ssm_chunk_fwd_workspace_bytes(int B, int T, int H, int HV, int K, int V, int N, int packed, int dtype) {
     if (B < 0 || T < 0 || H <= 0 || HV <= 0 || N < 0 || HV % H != 0 || (K != 64 && K != 128) || V <= 0 || V % 64 != 0 ||
-        !is_dtype(dtype))
+        !is_dtype(dtype) || (long long)B * T > SSM_MAX_ROWS)
         return 0;
     return kda::ssm_chunk_workspace(B, T, H, HV, K, V, packed ? N : B, packed != 0, dtype);
 }

@@ -853,7 +853,7 @@ Plan plan_of(int B, int T, int H, int HV, int K, int V, int N, bool packed, int 
     // (32768 tokens x 64 heads: 367 us, one slab a block 428)
     p.ns = dtype == KDA_BF16 && (p.slabs / H) % 2 == 0 ? 2 : 1;
     p.units = p.slabs / p.ns;
-    const long long chunks = (T + C - 1) / C;
+    const long long chunks = ((long long)T + C - 1) / C;
     long long seg = chunks > 0 ? chunks : 1;   // chunks of a segment
     if (packed) {
         // lengths are on the device: cut what is longer than twice an even share of the rows

@@ -456,8 +456,9 @@ size_t kda_conv_bwd_workspace_bytes(int B, int T, int D, int W, int N, int packe
  *   states     fp32 [N, HV, K, V]; final_state may be initial_state.
  *   K          64 or 128.   V: a multiple of 64.
  * x, b, c, y and the states must be 16-byte aligned, x_stride, b_stride and c_stride whole
- * 16-byte pieces, and a stride or row (HV V, HV K) under 2^24 elements. dt' is expected >= 0 (the softplus makes it so); a step's log2 decay is
- * taken as at least -200, where its exponential is 0 in fp32 either way.
+ * 16-byte pieces, a stride or row (HV V, HV K) under 2^24 elements, and B T at most
+ * 2^31 - 65. dt' is expected >= 0 (the softplus makes it so); a step's log2 decay is taken as
+ * at least -200, where its exponential is 0 in fp32 either way.
  *
  * kda_ssm_chunk_fwd is the prompt's form (chunks of 64 tokens on the matrix cores),
  * kda_ssm_recurrent_fwd walks tokens one by one (decode, short prompts).
