@@ -254,10 +254,14 @@ __device__ __forceinline__ float softplus_f32(float z) {
 __device__ __forceinline__ float ssm_step(float raw, float bias, int softplus) {
     return softplus ? softplus_f32(raw + bias) : raw + bias;
 }
-// a head's log2 decay for dt' = 1, and the log2 decay of a step; that is bounded at -200,
-// where its exponential is 0 all the same, so that sums of decays stay finite and their
-// differences exact enough
-__device__ __forceinline__ double ssm_rate(float A_log) { return -(double)expf(A_log) * 1.4426950408889634; }
-__device__ __forceinline__ double ssm_log2_decay(float dt, double rate) { return fmax((double)dt * rate, -200.0); }
+// v, at least `least`; NaN stays NaN (fmax would drop it)
+__device__ __forceinline__ double at_least(double v, double least) { return v < least ? least : v; }
+// a head's log2 decay for dt' = 1 (finite, so that a step of 0 keeps the state whatever A_log),
+// and the log2 decay of a step; that is bounded at -200, where its exponential is 0 all the
+// same, so that sums of decays stay finite and their differences exact enough
+__device__ __forceinline__ double ssm_rate(float A_log) {
+    return at_least(-exp((double)A_log) * 1.4426950408889634, -1e300);
+}
+__device__ __forceinline__ double ssm_log2_decay(float dt, double rate) { return at_least((double)dt * rate, -200.0); }
 
 }  // namespace kda

@@ -459,7 +459,7 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
     }
     if (FIRST) {
         store_slot(S, p.ends, p, w.slot0 + w.s, slab, wave);
-        if (threadIdx.x == 0) p.decay[(w.slot0 + w.s) * p.slabs + slab] = exp2_fast((float)fmax(total, -1000.0));
+        if (threadIdx.x == 0) p.decay[(w.slot0 + w.s) * p.slabs + slab] = exp2_fast((float)at_least(total, -1000.0));
     } else if (a.final_state && w.s == w.count - 1) {
         store_final(S, a, w.n, slab, 16 * wave + l16);
     }
@@ -795,7 +795,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
 #pragma unroll
         for (int u = 0; u < CT; ++u) store_slot(S[u], p.ends, p, w.slot0 + w.s, slab, part(u));
         if (mine < NS && lane == 0)
-            p.decay[(w.slot0 + w.s) * p.slabs + slab0 + mine] = exp2_fast((float)fmax(total, -1000.0));
+            p.decay[(w.slot0 + w.s) * p.slabs + slab0 + mine] = exp2_fast((float)at_least(total, -1000.0));
     } else if (a.final_state && w.s == w.count - 1) {
 #pragma unroll
         for (int u = 0; u < CT; ++u) store_final(S[u], a, w.n, slab, column(u));

@@ -52,6 +52,42 @@ def test_scan_operands_keep_16_bits(H, HV, K, V):
     near("y", y.view(T, HV, V), wy, (2.0 ** -16 * 1.01 + 16 * EPS) * my + OUT[BF] * 1.01 * np.abs(wy))
 
 
+@pytest.mark.parametrize("fn", SCANS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [50, 1500])
+def test_scan_a_nan_decay_is_nan(T, dtype, fn):
+    """A head whose A_log is NaN has NaN results, and no other head."""
+    c = ssm_case(5, dtype, 1, 4, 64, 64, T=T)
+    y, f = fn(**c, output_final_state=True)
+    c["A_log"] = c["A_log"].clone()
+    c["A_log"][1] = float("nan")
+    y2, f2 = fn(**c, output_final_state=True)
+    assert torch.isnan(y2[:, :, 1]).all() and torch.isnan(f2[:, 1]).all()
+    rest = [0, 2, 3]
+    assert torch.equal(y[:, :, rest], y2[:, :, rest]) and torch.equal(f[:, rest], f2[:, rest])
+
+
+@pytest.mark.parametrize("fn", SCANS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scan_extreme_decays(dtype, fn):
+    """exp(A_log) beyond fp32 with a step of 0 keeps the state, with any other erases it; an
+    infinite step erases it too, and A_log of -inf keeps it."""
+    T = 70
+    c = ssm_case(6, dtype, 1, 4, 64, 64, T=T, softplus=False, bias=False, dt_dtype=F32, D=False)
+    c["A_log"] = torch.tensor([90.0, 300.0, -float("inf"), 0.0], device=DEV)
+    c["dt"][:, :] = 0
+    y, f = fn(**c, output_final_state=True)
+    assert torch.equal(f, c["initial_state"])
+    c["dt"][:, 66, :2] = 1e-3          # heads 0, 1: everything before token 66 goes
+    c["dt"][:, 66, 3] = float("inf")   # head 3: the same, and what it writes is infinite or NaN
+    c["b"][:, 66] = 1.0
+    y2, f2 = fn(**c, output_final_state=True)
+    assert torch.equal(y[:, :66], y2[:, :66])
+    want = (c["dt"][:, 66, :2, None] * c["x"][:, 66, :2].float())[:, :, None, :].expand(-1, -1, 64, -1)
+    assert (f2[:, :2] - want).abs().max() <= 4 * EPS * want.abs().max()
+    assert torch.equal(f2[:, 2], f[:, 2]) and not torch.isfinite(f2[:, 3]).any()
+
+
 # ------------------------------------------------------------------------ the convolution
 def test_conv_longest_sequence():
     """The longest sequence there can be, one channel wide: its last rows against the
