@@ -165,11 +165,27 @@ def _bytes(name, workspace, need, dev):
     return workspace
 
 
-def _apart(name, out, inputs):
-    """An output a caller gives is none of the inputs that are read after it is written."""
-    for other, t in inputs:
-        if t is not None and out.data_ptr() == t.data_ptr() and out.numel():
-            raise ValueError(f"{name} must not be {other}")
+def _apart(name, out, others, same=()):
+    """A buffer a caller gives to be written shares no byte with the tensors in ``others``
+    (name, tensor or None, rows, elements between rows), except one named in ``same`` at its
+    very place, whose elements are read before they are written. Between rows that are apart there
+    may be other tensors."""
+    begin, size = out.data_ptr(), out.numel() * out.element_size()
+    for other, t, rows, stride in others:
+        if t is None or size == 0 or t.numel() == 0:
+            continue
+        at, item = t.data_ptr(), t.element_size()
+        if begin == at and other in same and t.is_contiguous():
+            continue
+        width, step = t.numel() // rows * item, stride * item
+        # the rows that end behind the buffer's begin and start ahead of its end
+        if max(0, (begin - at - width) // step + 1) <= min(rows - 1, (begin + size - 1 - at) // step):
+            raise ValueError(f"{name} must not overlap {other}")
+
+
+def _whole(**tensors):
+    """Contiguous tensors, as ``_apart`` takes them."""
+    return tuple((name, t, 1, 1) for name, t in tensors.items())
 
 
 def _size(t):
@@ -210,17 +226,21 @@ def kda_conv_fwd(x, weight, bias=None, initial_state=None, cu_seqlens=None, outp
     T = 1. ``out``, ``dev_status`` and ``debug`` as in ``kda_chunk_fwd``."""
     lib = _load()
     B, T, D, W, N, code, w_code, stride, dev = _conv_inputs(x, weight, bias, initial_state, cu_seqlens, activation)
+    if out is not None or final_state is not None:
+        inputs = (("x", x, B * T, stride), *_whole(weight=weight, bias=bias, initial_state=initial_state,
+                                                   cu_seqlens=cu_seqlens))
     if out is None:
         out = x.new_empty((B, T, D))
     else:
         _want("out", out, (B, T, D), (x.dtype,), dev)
-        _apart("out", out, (("x", x), ("initial_state", initial_state)))
+        _apart("out", out, inputs)
     if not output_final_state:
         final_state = None
     elif final_state is None:
         final_state = x.new_empty((N, W - 1, D))
     else:
         _want("final_state", final_state, (N, W - 1, D), (x.dtype,), dev)
+        _apart("final_state", final_state, inputs + _whole(out=out), same=("initial_state",))
     dev_status = _status(dev, dev_status, cu_seqlens, debug)
     _call(dev, lib.kda_conv_fwd, _at(x), stride, _at(weight), _at(bias), _at(initial_state), _at(cu_seqlens), N,
           _at(out), _at(final_state), B, T, D, W, code, w_code, _ACTIVATIONS[activation], _at(dev_status))
@@ -249,6 +269,10 @@ def kda_conv_bwd(dy, x, weight, bias=None, initial_state=None, cu_seqlens=None, 
     dweight = torch.empty(D, W, dtype=torch.float32, device=dev)
     dbias = torch.empty(D, dtype=torch.float32, device=dev) if bias is not None else None
     dinitial = new(N, W - 1, D, dtype=x.dtype, device=dev) if initial_state is not None else None
+    if workspace is not None:
+        _apart("workspace", workspace, (("x", x, B * T, stride),
+                                        *_whole(dy=dy, weight=weight, bias=bias, initial_state=initial_state,
+                                                cu_seqlens=cu_seqlens, dfinal_state=dfinal_state)))
     workspace = _bytes("workspace", workspace,
                        lib.kda_conv_bwd_workspace_bytes(B, T, D, W, N, int(cu_seqlens is not None), code), dev)
     dev_status = _status(dev, dev_status, cu_seqlens, debug)
@@ -280,23 +304,29 @@ def _ssm(chunk, x, dt, A_log, b, c, D, dt_bias, initial_state, cu_seqlens, outpu
     _want("D", D, (HV,), _F32, dev)
     _want("dt_bias", dt_bias, (HV,), _F32, dev)
     _want("initial_state", initial_state, (N, HV, K, V), _F32, dev)
+    if out is not None or final_state is not None or workspace is not None:
+        inputs = (*((name, t, B * T, s) for (name, t), s in zip((("x", x), ("dt", dt), ("b", b), ("c", c)), strides)),
+                  *_whole(A_log=A_log, D=D, dt_bias=dt_bias, initial_state=initial_state, cu_seqlens=cu_seqlens))
     if out is None:
         out = x.new_empty((B, T, HV, V))
     else:
         _want("out", out, (B, T, HV, V), (x.dtype,), dev)
-        _apart("out", out, (("x", x), ("b", b), ("c", c), ("dt", dt)))
+        _apart("out", out, inputs)
     if not output_final_state:
         final_state = None
     elif final_state is None:
         final_state = A_log.new_empty((N, HV, K, V))
     else:
         _want("final_state", final_state, (N, HV, K, V), _F32, dev)
+        _apart("final_state", final_state, inputs + _whole(out=out), same=("initial_state",))
     dev_status = _status(dev, dev_status, cu_seqlens, debug)
     args = [_at(x), strides[0], _at(dt), strides[1], _at(A_log), _at(b), strides[2], _at(c), strides[3], _at(D),
             _at(dt_bias), _at(initial_state), _at(cu_seqlens), N, _at(out), _at(final_state), B, T, H, HV, K, V, code,
             dt_code, int(bool(dt_softplus))]
     if chunk:
         need = lib.kda_ssm_chunk_fwd_workspace_bytes(B, T, H, HV, K, V, N, int(cu_seqlens is not None), code)
+        if workspace is not None:
+            _apart("workspace", workspace, inputs + _whole(out=out, final_state=final_state))
         workspace = _bytes("workspace", workspace, need, dev)
         _call(dev, lib.kda_ssm_chunk_fwd, *args, _at(workspace), _size(workspace), _at(dev_status))
     else:
@@ -356,21 +386,27 @@ def kda_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, output_rstd=False, ou
     """RMS norm over the last axis of h = x + residual (x alone without one). Returns
     ``(y, h or None, rstd or None)``: y = h (mean h^2 + eps)^-1/2 weight and h in x's dtype
     (h only with a residual), rstd float32 [...] with ``output_rstd`` (the backward's
-    input). ``residual_out`` may be ``residual``, ``out`` may be ``x``."""
+    input). ``out`` and ``residual_out`` may each be ``residual`` or, where it is contiguous,
+    ``x``, but not the same one."""
     lib = _load()
     shape, rows, D, code, w_code, stride, dev = _norm_inputs(x, weight, residual)
     if out is None:
         out = x.new_empty(shape)
     else:
         _want("out", out, shape, (x.dtype,), dev)
-    h = _sum_buffer(shape, x, residual, residual_out, dev)
+        _apart("out", out, _norm_reads(x, rows, stride, weight, residual), same=("x", "residual"))
+    h = _sum_buffer(shape, x, rows, stride, weight, residual, residual_out, dev, out=out)
     rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if output_rstd else None
     _call(dev, lib.kda_rmsnorm_fwd, _at(x), stride, _at(weight), _at(residual), _at(out), _at(h), _at(rstd), rows, D,
           eps, code, w_code)
     return out, h, rstd
 
 
-def _sum_buffer(shape, x, residual, residual_out, dev):
+def _norm_reads(x, rows, stride, weight, residual):
+    return (("x", x, rows, stride), *_whole(weight=weight, residual=residual))
+
+
+def _sum_buffer(shape, x, rows, stride, weight, residual, residual_out, dev, **outputs):
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out belongs to a residual")
@@ -378,6 +414,7 @@ def _sum_buffer(shape, x, residual, residual_out, dev):
     if residual_out is None:
         return x.new_empty(shape)
     _want("residual_out", residual_out, shape, (x.dtype,), dev)
+    _apart("residual_out", residual_out, _norm_reads(x, rows, stride, weight, residual) + _whole(**outputs), same=("x", "residual"))
     return residual_out
 
 
@@ -397,11 +434,13 @@ def kda_rmsnorm_quant_fwd(x, weight, residual=None, *, eps=1e-6, group=0, out=No
         out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
     else:
         _want("out", out, shape, (torch.float8_e4m3fn,), dev)
+        _apart("out", out, _norm_reads(x, rows, stride, weight, residual))
     if scales is None:
         scales = torch.empty(sshape, dtype=torch.float32, device=dev)
     else:
         _want("scales", scales, sshape, _F32, dev)
-    h = _sum_buffer(shape, x, residual, residual_out, dev)
+        _apart("scales", scales, _norm_reads(x, rows, stride, weight, residual) + _whole(out=out))
+    h = _sum_buffer(shape, x, rows, stride, weight, residual, residual_out, dev, out=out, scales=scales)
     _call(dev, lib.kda_rmsnorm_quant_fwd, _at(x), stride, _at(weight), _at(residual), _at(out), _at(scales), _at(h),
           rows, D, group or D, eps, code, w_code)
     return out, scales, h
@@ -425,6 +464,8 @@ def kda_rmsnorm_bwd(dy, h, weight, rstd, dh=None, *, workspace=None):
     _want("rstd", rstd, shape[:-1], _F32, dev)
     dx = h.new_empty(shape)
     dweight = torch.empty(D, dtype=torch.float32, device=dev)
+    if workspace is not None:
+        _apart("workspace", workspace, _whole(dy=dy, h=h, weight=weight, rstd=rstd, dh=dh))
     workspace = _bytes("workspace", workspace, lib.kda_rmsnorm_bwd_workspace_bytes(rows, D, code), dev)
     _call(dev, lib.kda_rmsnorm_bwd, _at(dy), _at(h), _at(weight), _at(rstd), _at(dh), _at(dx), _at(dweight), rows, D,
           code, w_code, _at(workspace), _size(workspace))

@@ -486,8 +486,8 @@ int kda_ssm_recurrent_fwd(const void* x, long long x_stride, const void* dt, lon
  * RMS norm over the last axis with the residual's addition:
  *     h = x + residual (x without one),  r = (mean h^2 + eps)^(-1/2),  y = h r weight
  *   x          rows of D, x_stride elements apart; residual, h and y [rows, D] in dtype.
- *   h          NULL, or receives h in dtype; the norm uses the fp32 sum. h may be residual,
- *              y may be x (when x is contiguous).
+ *   h          NULL, or receives h in dtype; the norm uses the fp32 sum. h and y may each be
+ *              residual or (when it is contiguous) x, but not the same one.
  *   rstd       NULL, or fp32 [rows] receiving r (the backward's input).
  * kda_rmsnorm_quant_fwd leaves q uint8 [rows, D] instead of y: OCP e4m3 codes of y / s and
  * s fp32 [rows, D / group] with s = max(max |y|, 2^-110) / 448 over the group's columns

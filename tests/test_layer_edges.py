@@ -2,6 +2,7 @@
 import os
 
 import pytest
+import torch
 
 import gated_delta_rule_64_amd as kda
 from gated_delta_rule_64_amd import _layer, _lib
@@ -34,3 +35,25 @@ def test_scan_rows_are_bounded(lib):
     assert size(1, most + 1, 1, 1, 64, 64, 1, 0, 1) == 0
     # dt' and the two sums of every row at least
     assert size(1, most, 1, 1, 64, 64, 1, 0, 1) >= size(1, most - 64, 1, 1, 64, 64, 1, 0, 1) >= 12 * (most - 64)
+
+
+def test_overlap_is_by_bytes():
+    """The binding's check of given outputs, on host tensors."""
+    buf = torch.zeros(1000)
+
+    def hits(out, t, rows=1, stride=1, same=()):
+        try:
+            _layer._apart("out", out, (("t", t, rows, stride),), same)
+        except ValueError:
+            return True
+        return False
+    t = buf[100:200]
+    for a, b, want in ((0, 100, False), (0, 101, True), (199, 300, True), (200, 300, False), (150, 150, False), (0, 1000, True),
+                       (120, 130, True)):
+        assert hits(buf[a:b], t) is want
+    assert hits(buf[100:200], t) and not hits(buf[100:200], t, same=("t",)) and hits(buf[101:201], t, same=("t",))
+    assert not hits(t, None) and not hits(t, buf[150:150])
+    rows = buf.as_strided((5, 10), (100, 1), 200)     # elements 200.., 300.., .. 600..609
+    for a, b, want in ((0, 200, False), (0, 201, True), (210, 300, False), (209, 300, True), (210, 301, True), (610, 700, False),
+                       (609, 700, True), (550, 560, False), (450, 560, True)):
+        assert hits(buf[a:b], rows, 5, 100) is want, (a, b)

@@ -139,3 +139,62 @@ def test_norm_codes_are_those_of_the_quotient(group, dtype):
     assert torch.equal(s.cpu().view(ws.shape), ws)
     want = (y.view(rows, -1, group or D) / ws[..., None]).to(torch.float8_e4m3fn).view(rows, D)
     assert torch.equal(q.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+# ------------------------------------------------------------------------- outputs given
+def test_overlapping_outputs_are_refused():
+    def refused(f, *a, **k):
+        with pytest.raises(ValueError, match="overlap"):
+            f(*a, **k)
+    c = conv_case(60, BF, BF, 4, 64, B=2, T=40)
+    flat = torch.zeros(3 * 5120, dtype=BF, device=DEV)
+    c["x"] = flat[:5120].view(2, 40, 64)
+    out = flat[5120:10240].view(2, 40, 64)
+    refused(kda.kda_conv_fwd, **c, out=flat[5056:10176].view(2, 40, 64))             # x's last row
+    refused(kda.kda_conv_fwd, **c, output_final_state=True, final_state=flat[:384].view(2, 3, 64))
+    refused(kda.kda_conv_fwd, **c, out=out, output_final_state=True, final_state=flat[9856:10240].view(2, 3, 64))
+    refused(kda.kda_conv_bwd, out, **c, workspace=flat[5120:10240])
+    kda.kda_conv_fwd(**c, out=out, output_final_state=True, final_state=c["initial_state"])
+    kda.kda_conv_fwd(**c, out=out, output_final_state=True, final_state=flat[10240:10624].view(2, 3, 64))
+    states = torch.zeros(2 * 16384, device=DEV)
+    s = ssm_case(61, BF, 1, 2, 64, 64, T=40, B=2)
+    s["initial_state"] = states[:16384].view(2, 2, 64, 64)
+    for f in SCANS:
+        refused(f, **s, output_final_state=True, final_state=states[64:64 + 16384].view(2, 2, 64, 64))
+        refused(f, **s, out=s["x"])
+        f(**s, output_final_state=True, final_state=s["initial_state"])
+        f(**s, output_final_state=True, final_state=states[16384:].view(2, 2, 64, 64))
+    refused(kda.kda_ssm_chunk_fwd, **s, workspace=states)
+    both = torch.zeros(2 * 16384, device=DEV)
+    s = ssm_case(62, F32, 1, 2, 64, 64, T=128)
+    for f in SCANS:
+        refused(f, **s, out=both[:16384].view(1, 128, 2, 64), output_final_state=True, final_state=both[8192:16384].view(1, 2, 64, 64))
+    # between the rows of a wider tensor there is room for others
+    wide = torch.zeros(3, 4096, dtype=BF, device=DEV)
+    x, w = wide[:, :64], randn(gen(66), 64, dtype=BF)
+    kda.kda_rmsnorm_fwd(x, w, out=wide[1, 64:256].view(3, 64))
+    refused(kda.kda_rmsnorm_fwd, x, w, out=wide[1, 63:255].view(3, 64))
+    refused(kda.kda_rmsnorm_fwd, x, w, out=wide.view(-1)[2 * 4096 - 191:2 * 4096 + 1].view(3, 64))
+    kda.kda_rmsnorm_fwd(x, w, out=wide.view(-1)[2 * 4096 - 192:2 * 4096].view(3, 64))
+    # the norms
+    n, w = randn(gen(63), 9, 512, dtype=BF), randn(gen(64), 256, dtype=BF)
+    x, res = n[:, :256], randn(gen(65), 9, 256, dtype=BF)
+    over = n.view(-1)[:9 * 256].view(9, 256)
+    t = torch.empty(9, 256, dtype=BF, device=DEV)
+    for f in (kda.kda_rmsnorm_fwd, kda.kda_rmsnorm_quant_fwd):
+        refused(f, x, w, res, residual_out=over)
+    refused(kda.kda_rmsnorm_fwd, x, w, res, out=over)
+    refused(kda.kda_rmsnorm_fwd, x, w, res, out=t, residual_out=t)
+    refused(kda.kda_rmsnorm_fwd, x, w, res, out=res, residual_out=res)
+    refused(kda.kda_rmsnorm_fwd, x[:1], w, out=w.view(1, 256))
+    q = torch.empty(9, 256, dtype=torch.float8_e4m3fn, device=DEV)
+    refused(kda.kda_rmsnorm_quant_fwd, x, w, out=q, scales=q.view(torch.uint8).view(-1)[:36].view(torch.float32).view(9, 1))
+    refused(kda.kda_rmsnorm_quant_fwd, x, w, res, out=res.view(torch.uint8).view(-1)[:2304].view(9, 256).view(torch.float8_e4m3fn))
+    refused(kda.kda_rmsnorm_bwd, t, res, w, torch.ones(9, device=DEV), workspace=res)
+    # in place, row for row: each of y and h over either input
+    a = x.contiguous()
+    y, h, _ = kda.kda_rmsnorm_fwd(a, w, res)
+    for swap in (False, True):
+        b, r = a.clone(), res.clone()
+        y2, h2, _ = kda.kda_rmsnorm_fwd(b, w, r, out=r if swap else b, residual_out=b if swap else r)
+        assert torch.equal(y, y2) and torch.equal(h, h2)
