@@ -316,6 +316,8 @@ template <int KT> __device__ __forceinline__ void store_final(const f32x4 (&S)[K
         for (int r = 0; r < 4; ++r) hT[(size_t)(16 * t + 4 * g + r) * a.V] = S[t][r];
 }
 
+__device__ __forceinline__ bool is_finite(float v) { return fabsf(v) < __builtin_inff(); }
+
 // ---------------------------------------------------------------------------------
 // fp32 inputs: everything on the fp32 matrix cores, one slab a block. FIRST: the first
 // pass, which only carries the state.
@@ -408,6 +410,19 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
 #pragma unroll
             for (int r = 0; r < 4; ++r) xt[J][r] = Xs[(16 * J + 4 * g + r) * LDX + 16 * wave + l16];
         if constexpr (!FIRST) {
+            // see `odd` of the bf16 kernel
+            float zero = 0.f;
+#pragma unroll
+            for (int J = 0; J < 4; ++J)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) zero = fmaf(xt[J][r], 0.f, zero);
+            const bool odd = __any(zero != zero);
+            if (odd) {
+#pragma unroll
+                for (int J = 0; J < 4; ++J)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) xt[J][r] = is_finite(xt[J][r]) ? xt[J][r] : 0.f;
+            }
             __syncthreads();
 #pragma unroll
             for (int I = 0; I < 4; ++I) {
@@ -431,13 +446,29 @@ __global__ __launch_bounds__(256) void ssm_scan_f32_kernel(const SsmArgs a, cons
 #pragma unroll
                     for (int r = 0; r < 4; ++r) acc = Mma<float>::mma(xt[J][r], m[r], acc);
                 }
+                const int q = 16 * wave + 4 * g;
+                if (odd) {
+                    for (int j = 0; j <= i; ++j) {
+                        const float m = Ms[(I * (I + 1) / 2 + (j >> 4)) * 64 + (j >> 2 & 3) * 16 + l16][j & 3];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float v = Xs[j * LDX + q + r];
+                            if (!is_finite(v)) acc[r] = fmaf(m, v, acc[r]);
+                        }
+                    }
+                }
                 if (i < cl) {   // columns 16 wave + 4 g .. +3 of token i
-                    const int q = 16 * wave + 4 * g;
                     float out[4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) out[r] = fmaf(skip, Xs[i * LDX + q + r], acc[r]);
                     store_vec<4>(static_cast<float*>(a.y) + ((row + i) * p.slabs + slab) * (long long)SLAB + q, out);
                 }
+            }
+            if (odd) {
+#pragma unroll
+                for (int J = 0; J < 4; ++J)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) xt[J][r] = Xs[(16 * J + 4 * g + r) * LDX + 16 * wave + l16];
             }
         }
         // the state at the chunk's end
@@ -659,14 +690,36 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
             if (p0 + 2 * C < stop) fetch_steps(p0 + 2 * C);
         }
         // this wave's columns of x down the tokens
+        auto column_of_x = [&](int u, int s) {
+            return join(read_col4<LDX>(Xs[q] + colx + 4 * u, 2 * s), read_col4<LDX>(Xs[q] + colx + 4 * u, 2 * s + 1));
+        };
         bf16x8 xf[CT][2];
 #pragma unroll
         for (int u = 0; u < CT; ++u)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                xf[u][s] = join(read_col4<LDX>(Xs[q] + colx + 4 * u, 2 * s), read_col4<LDX>(Xs[q] + colx + 4 * u, 2 * s + 1));
+                xf[u][s] = column_of_x(u, s);
         f32x4 acc[FIRST ? 1 : CT][FIRST ? 1 : 4];
         if constexpr (!FIRST) {
+            // A NaN or infinity among this wave's x: M's zeros above the diagonal times it would
+            // reach the tokens before it. Such values are left out of M x and come in one by one,
+            // for the tokens from their own on (and are back for the state's update). Found by a
+            // product with 0 on the matrix cores (1% of the pass).
+            f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < CT; ++u)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) zero = mma32(bf16x8{}, xf[u][s], zero);
+            const bool odd = __any(zero[0] != zero[0]);
+            if (odd) {
+#pragma unroll
+                for (int u = 0; u < CT; ++u)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (!is_finite((float)xf[u][s][e])) xf[u][s][e] = (__bf16)0.f;
+            }
             // M^T's ten tiles (token rows J, columns I >= J), three or two a wave: 4 bits of
             // I and J each, the first tile lowest
             static_assert(WAVES == 4, "M's tiles are dealt to four waves");
@@ -745,6 +798,19 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
 #pragma unroll
                     for (int u = 0; u < CT; ++u) acc[u][I] = mma32(xf[u][s], mh, acc[u][I]);
                 }
+                if (odd) {
+                    const int i = 16 * I + l16;
+                    for (int j = 0; j <= i; ++j) {
+                        const __bf16* mj = Ms[q] + (m_tile(I, j >> 4) * 64 + (j >> 2 & 3) * 16 + l16) * 8 + (j & 3);
+                        const float m = (float)mj[0] + (float)mj[4];
+                        const __bf16* xj = Xs[q] + row_at<LDX>(j) + base + 4 * CT * g;
+#pragma unroll
+                        for (int e = 0; e < 4 * CT; ++e) {
+                            const float v = (float)xj[e];
+                            if (!is_finite(v)) acc[e >> 2][I][e & 3] = fmaf(m, v, acc[e >> 2][I][e & 3]);
+                        }
+                    }
+                }
                 // columns base + 4 NS g .. of token 16 I + l % 16
                 const __bf16* xi = Xs[q] + row_at<LDX>(l16) + base + 4 * CT * g + row_at<LDX>(16 * I);
                 if constexpr (CT == 2) {
@@ -760,6 +826,12 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 4 : 2) void ssm_scan_bf16_
                     for (int e = 0; e < 4; ++e) out[e] = (__bf16)fmaf(skip, (float)x4[e], acc[0][I][e]);
                     __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, out), yd, y_at + I * 16 * y_row, 0, 0);
                 }
+            }
+            if (odd) {
+#pragma unroll
+                for (int u = 0; u < CT; ++u)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) xf[u][s] = column_of_x(u, s);
             }
         }
         // the state at the chunk's end

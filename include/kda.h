@@ -400,8 +400,8 @@ size_t kda_noalloc_scratch_bytes(void);
  *     consecutive rows (tokens; row b T + t) are `*_stride` elements apart and contiguous
  *     inside. Every other tensor is contiguous.
  *   - dtype is KDA_BF16 or KDA_F32 for the activations; arithmetic, sums and states are fp32.
- *   - A NaN or infinity in a token never reaches another sequence. kda_ssm_chunk_fwd may let
- *     it reach earlier outputs of its own 64-token chunk (0 times NaN in a matrix product).
+ *   - A NaN or infinity in a token never reaches an earlier one or another sequence. From its
+ *     token on, kda_ssm_chunk_fwd may give NaN where the token by token form gives an infinity.
  *   - No output may overlap an input, except where that is said.
  *   - kda_conv_fwd, kda_conv_bwd and kda_ssm_chunk_fwd find a packed batch's tiles by searching
  *     the offsets. Where a slot's offsets are broken, that slot is skipped and flagged as

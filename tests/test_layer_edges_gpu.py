@@ -88,6 +88,37 @@ def test_scan_extreme_decays(dtype, fn):
     assert torch.equal(f2[:, 2], f[:, 2]) and not torch.isfinite(f2[:, 3]).any()
 
 
+@pytest.mark.parametrize("fn", SCANS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,HV,K,V", [(1, 2, 64, 64), (2, 2, 64, 64), (1, 2, 128, 128)])
+def test_scan_odd_values_reach_nothing_before_them(H, HV, K, V, dtype, fn):
+    """A NaN or an infinity in any input of a token leaves every earlier output and, in x, every
+    other column as they were."""
+    T = 200
+    c = ssm_case(7, dtype, H, HV, K, V, T=T)
+    y, f = fn(**c, output_final_state=True)
+    for name in ("x", "b", "c", "dt"):
+        for at in (0, 5, 15, 16, 63, 64, 77, 130, 199):
+            for bad in (float("nan"), float("inf")):
+                d = {**c, name: c[name].clone()}
+                if name == "x":
+                    d["x"][0, at, 0, 3] = bad
+                else:
+                    d[name][0, at] = bad
+                y2, f2 = fn(**d, output_final_state=True)
+                assert torch.equal(y2[:, :at], y[:, :at]), (name, at, bad)
+                if name == "c":
+                    assert torch.equal(y2[:, at + 1:], y[:, at + 1:]) and torch.equal(f2, f)
+                    assert not torch.isfinite(y2[:, at]).any()
+                elif name == "x":
+                    other = torch.ones(HV, V, dtype=torch.bool, device=DEV)
+                    other[0, 3] = False
+                    assert torch.equal(y2[0][:, other], y[0][:, other]) and torch.equal(f2[0].transpose(1, 2)[other], f[0].transpose(1, 2)[other])
+                    assert not torch.isfinite(y2[0, at, 0, 3]) and not torch.isfinite(f2[0, 0, :, 3]).any()
+                elif name == "b" or bad != bad:
+                    assert not torch.isfinite(y2[:, at]).any()
+
+
 # ------------------------------------------------------------------------ the convolution
 def test_conv_longest_sequence():
     """The longest sequence there can be, one channel wide: its last rows against the
