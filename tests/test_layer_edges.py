@@ -57,3 +57,31 @@ def test_overlap_is_by_bytes():
     for a, b, want in ((0, 200, False), (0, 201, True), (210, 300, False), (209, 300, True), (210, 301, True), (610, 700, False),
                        (609, 700, True), (550, 560, False), (450, 560, True)):
         assert hits(buf[a:b], rows, 5, 100) is want, (a, b)
+
+
+def test_scan_bounds_see_a_dropped_part():
+    """What the bounds of the GPU tests of the scan's writes and decays are made to see: a weighted x
+    cut into two bf16 instead of three, and running sums of decays without their low part."""
+    eps = 2.0 ** -24
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(1000, generator=g).bfloat16().float()
+    v = (torch.rand(1000, generator=g) + 0.5) * x
+
+    def cut(v, parts):
+        left, total = v.clone(), torch.zeros_like(v, dtype=torch.float64)
+        for _ in range(parts):
+            top = (left.view(torch.int32) & -65536).view(torch.float32)
+            total += top.double()
+            left = left - top
+        return total
+    off = lambda t: ((t - v.double()).abs() / v.double().abs()).max().item()  # noqa: E731
+    assert off(cut(v, 3)) == 0 and off(cut(v, 2)) > 4 * 40 * eps      # 40: the widest of test_scan_writes_are_fp32_products
+    # sixteen decays of 131 log2(e), then some of 0.01: 2^(last - sum at the write) from the sums
+    steps = torch.cat([torch.full((16,), 131.0), 0.001 + 0.01 * torch.rand(48, generator=g)])
+    cum = torch.cumsum(steps.double() * -1.4426950408889634, 0)
+    want = torch.exp2(cum[-1] - cum[16])
+    hi = cum.float()
+    lo = (cum - hi.double()).float()
+    both = torch.exp2((hi[-1] - hi[16]).double() + (lo[-1] - lo[16]).double())
+    assert abs(both - want) <= 2 * eps * want
+    assert abs(torch.exp2((hi[-1] - hi[16]).double()) - want) > 4 * 16 * eps * want

@@ -54,6 +54,62 @@ def test_scan_operands_keep_16_bits(H, HV, K, V):
 
 @pytest.mark.parametrize("fn", SCANS)
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H,HV,V,T", [(1, 2, 64, 64), (2, 2, 64, 40), (1, 2, 128, 1000)])
+def test_scan_writes_are_fp32_products(H, HV, V, T, dtype, fn):
+    """Token t writes row t % K alone and nothing decays (dt' x b summed over a few tokens): a
+    state element is a sum of at most T / K + 1 fp32 products."""
+    K = 64
+    c = ssm_case(3, dtype, H, HV, K, V, T=T, state=False, softplus=False, bias=False, dt_dtype=F32, a_log=-np.inf)
+    t = torch.arange(T, device=DEV)
+    keep = torch.zeros(T, K, device=DEV, dtype=dtype)
+    keep[t, t % K] = 1
+    c["b"] *= keep[None, :, None]
+    _, final = fn(**c, output_final_state=True)
+    _, wf, _, mf = scan_oracle(c)
+    # dt' x, its product with b (three parts of it, added one by one, in the chunked form), the sum
+    near("final", final, wf, (8 + 2 * (T // K + 1)) * EPS * mf + 1e-37)
+
+
+@pytest.mark.parametrize("fn", SCANS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scan_decays_far_along_a_chunk(dtype, fn):
+    """Sixteen tokens of 189 log2 units of decay each, then a write, then little decay: the
+    differences of the running sums must keep what a sum near 3000 rounded to fp32 (2e-4) loses."""
+    c = ssm_case(4, dtype, 1, 2, 64, 64, T=64, softplus=False, bias=False, dt_dtype=F32, a_log=0.0)
+    c["dt"][:, :16] = 131.0
+    c["dt"][:, 16:] = c["dt"][:, 16:] * 0.01 + 0.001
+    c["x"][:, :16] = 0
+    c["x"][:, 17:] = 0
+    y, final = fn(**c, output_final_state=True)
+    wy, wf, my, mf = scan_oracle(c)
+    # E < 2 log2 units over the last 47 tokens: the exponent's rounding E EPS, 2 EPS an exponential
+    # and a rounding a product, one factor a token in the per-token form
+    rel = (16 if fn is kda.kda_ssm_chunk_fwd else 4 * 48 + 16) * EPS
+    near("final", final, wf, rel * mf + 1e-37)
+    if dtype == F32:
+        near("y", y.view(64, 2, 64), wy, (rel + 70 * EPS) * my + 1e-37)
+
+
+@pytest.mark.parametrize("fn", SCANS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_scan_softplus(dtype, fn):
+    """One token of x = b = 1 leaves dt' itself in the state: softplus within 9 half steps from
+    where it underflows to where it is its argument."""
+    B, HV = 512, 8
+    z = torch.cat([torch.linspace(-86, 0, B * HV // 2), torch.linspace(0, 30, B * HV // 2 - 4), torch.tensor([199.9, 200.0, 250.0, 1e30])])
+    ones = lambda *s: torch.ones(*s, dtype=dtype, device=DEV)  # noqa: E731
+    _, final = fn(ones(B, 1, HV, 64), z.view(B, 1, HV).to(DEV), torch.zeros(HV, device=DEV), ones(B, 1, 1, 64), ones(B, 1, 1, 64),
+                  output_final_state=True, dt_softplus=True)
+    want = layer.softplus(f64(z)).reshape(B, HV, 1, 1)
+    # the bf16 scan takes dt' x in three bf16 parts, under 1, 2^-7 and 2^-15 of it; the matrix cores
+    # take a part below the smallest normal number as 0, which loses less than 2^-126 for each
+    # of the two that a normal product can have there
+    lost = 2 * 2.0 ** -126 if dtype == BF and fn is kda.kda_ssm_chunk_fwd else 0.0
+    near("dt'", final, np.broadcast_to(want, final.shape), np.broadcast_to(9 * EPS * want + lost, final.shape))
+
+
+@pytest.mark.parametrize("fn", SCANS)
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T", [50, 1500])
 def test_scan_a_nan_decay_is_nan(T, dtype, fn):
     """A head whose A_log is NaN has NaN results, and no other head."""
@@ -119,6 +175,19 @@ def test_scan_odd_values_reach_nothing_before_them(H, HV, K, V, dtype, fn):
                     assert not torch.isfinite(y2[:, at]).any()
 
 
+def test_scan_more_segments_than_are_sorted():
+    """A packed batch of more than 4096 segments, which the second pass takes as they come."""
+    lens = [int(v) for v in np.random.default_rng(8).integers(0, 4, 4500)] + [300, 0, 2]
+    c = ssm_case(8, BF, 1, 1, 64, 64, lens=lens, tail=3)
+    y, f = kda.kda_ssm_chunk_fwd(**c, output_final_state=True, debug=True)
+    y2, f2 = kda.kda_ssm_recurrent_fwd(**c, output_final_state=True)
+    wy, wf, my, mf = scan_oracle(c)
+    steps = (300 + 64 + 1400) * EPS
+    for a, b in ((y, f), (y2, f2)):
+        near("y", a.view(-1, 1, 64)[:sum(lens)], wy[:sum(lens)], ((steps + OUT[BF]) * my + OUT[BF] * 1.01 * np.abs(wy))[:sum(lens)])
+        near("final", b, wf, steps * mf + 1e-35)
+
+
 # ------------------------------------------------------------------------ the convolution
 def test_conv_longest_sequence():
     """The longest sequence there can be, one channel wide: its last rows against the
@@ -142,6 +211,32 @@ def test_conv_longest_sequence():
     assert torch.equal(dx[:, -1000:], wx) and not dx[:, :1 << 20].any()
     # the same 1000 terms, added in another order
     near("dw", dw, f64(ww), 2 * 1004 * EPS * 1.1 * np.abs(f64(dy[:, -1000:])).sum() * np.abs(f64(tail)).max())
+
+
+def conv_sums_case(i):
+    rng = np.random.default_rng(20 + i)
+    return [dict(dtype=F32, wdtype=F32, W=4, D=256, B=1, T=34000),
+            dict(dtype=BF, wdtype=BF, W=3, D=200, lens=[int(v) for v in rng.integers(0, 90, 800)], tail=7),
+            dict(dtype=BF, wdtype=F32, W=4, D=252, lens=[1, 0, 2] * 400 + [9000, 63, 64, 65], tail=1)][i]
+
+
+@pytest.mark.parametrize("i", range(3))
+def test_conv_backward_of_many_tiles_a_block(i):
+    """So many rows of so few channels that a block walks several tiles, the last round uneven."""
+    c = conv_case(30 + i, **conv_sums_case(i))
+    B, T, D = c["x"].shape
+    dy = randn(gen(40 + i), B, T, D, dtype=c["x"].dtype)
+    dx, dw, db, dh = kda.kda_conv_bwd(dy, **c, activation=None)
+    seqs = layer.spans(B, T, None if c["cu_seqlens"] is None else c["cu_seqlens"].tolist())
+    *want, mag = layer.conv_bwd(f64(dy).reshape(T, D), f64(c["x"]).reshape(T, D), f64(c["weight"]), f64(c["bias"]),
+                                f64(c["initial_state"]), None, seqs, False)
+    out = OUT[c["x"].dtype] * 1.01
+    live = ~np.isnan(want[0][:, 0])
+    near("dx", dx.view(T, D)[torch.tensor(live, device=DEV)], want[0][live], 6 * EPS * mag[0][live] + out * np.abs(want[0][live]))
+    # each tile of 64 rows is summed in fp32, the tiles' sums beyond it
+    near("dw", dw, want[1], 70 * EPS * mag[1])
+    near("db", db, want[2], 70 * EPS * mag[2])
+    near("dinitial", dh, want[3], 6 * EPS * mag[3] + out * np.abs(want[3]))
 
 
 # ------------------------------------------------------------------------------ the norm
