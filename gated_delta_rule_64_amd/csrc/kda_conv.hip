@@ -83,9 +83,10 @@ __device__ __forceinline__ void load_row(const ConvArgs& a, const SeqTile& s, in
 template <typename T, int VEC, int W>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvArgs a, int along, int dblocks, long long tiles,
                                                        int tiles_dense) {
-    if (blockIdx.x == 0) flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
-    const int dv = (int)(blockIdx.x % dblocks) * along + (threadIdx.x & (along - 1));
-    const long long tile = (long long)(blockIdx.x / dblocks) * (256 / along) + threadIdx.x / along;
+    const unsigned block = block_number();
+    if (block == 0) flag_bad_offsets(a.cu_seqlens, a.N, a.T, a.dev_status);
+    const int dv = (int)(block % dblocks) * along + (threadIdx.x & (along - 1));
+    const long long tile = (long long)(block / dblocks) * (256 / along) + threadIdx.x / along;
     const int d = dv * VEC;
     if (d >= a.D || tile >= tiles) return;
     const SeqTile s = seq_tile(tile, a.cu_seqlens, a.N, a.T, TT_FWD, tiles_dense);
@@ -280,7 +281,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvBwdArgs b, int 
 __global__ __launch_bounds__(1024) void sum_rows_kernel(const SumRows s) {
     __shared__ float part[32][33];
     const int ln = threadIdx.x & 31, q = threadIdx.x >> 5;
-    const long long m = (long long)blockIdx.x * 32 + ln;
+    const long long m = (long long)block_number() * 32 + ln;
     float acc = 0.f;
     if (m < s.M) {
         const long long each = (s.P + 31) / 32;
@@ -325,7 +326,7 @@ hipError_t fwd_v(const ConvArgs& a) {
     if (blocks == 0) return hipSuccess;
     if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
     const int td = tiles_dense_of(a.T, TT_FWD);
-    const dim3 grid((unsigned)blocks), block(256);
+    const dim3 grid = grid_of(blocks, 256), block(256);
     if (a.W == 4) hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, 4>), grid, block, 0, a.stream, a, along, dblocks, tiles, td);
     else if (a.W == 3) hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, 3>), grid, block, 0, a.stream, a, along, dblocks, tiles, td);
     else hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, 2>), grid, block, 0, a.stream, a, along, dblocks, tiles, td);
@@ -341,7 +342,7 @@ hipError_t bwd_v(const ConvBwdArgs& b) {
     const int groups = 256 / along;
     const long long P = bwd_rows_of_blocks(tiles, groups);
     const long long blocks = P * dblocks;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
     const int td = tiles_dense_of(a.T, TT_BWD);
     const dim3 grid((unsigned)blocks), block(256);
     const size_t lds = (size_t)256 * VEC * (a.W + 1) * sizeof(float);
@@ -359,7 +360,7 @@ hipError_t bwd_v(const ConvBwdArgs& b) {
 }  // namespace
 
 hipError_t launch_sum_rows(const SumRows& s, hipStream_t stream) {
-    hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((s.M + 31) / 32)), dim3(1024), 0, stream, s);
+    hipLaunchKernelGGL(sum_rows_kernel, grid_of((s.M + 31) / 32, 1024), dim3(1024), 0, stream, s);
     return hipGetLastError();
 }
 

@@ -13,6 +13,10 @@ namespace kda {
 // layer's error path, shared with the entry points that live in other files).
 int set_error(int code, const char* fmt, ...);
 
+// Whether a launch of `blocks` blocks of `threads` along one dimension is one that HIP makes: it
+// counts the dimension's threads in 32 bits and drops what is above, mostly without an error.
+inline bool grid_fits(long long blocks, int threads) { return blocks * threads <= 0xffffffffLL; }
+
 // How the loads obtain the per-token log2 decay (the public kda_gate values).
 enum GateMode {
     GATE_LOG2 = KDA_GATE_LOG2,           // g: fp32 per-token log2 decay, as given

@@ -94,6 +94,13 @@ inline bool rows_of_16_bytes(int dtype, int D, long long stride) {
     const int vec = dtype == KDA_BF16 ? 8 : 4;
     return D % vec == 0 && stride % vec == 0;
 }
+// a grid of at least `blocks` blocks (under 2^31), the further ones along y; see grid_fits
+inline dim3 grid_of(long long blocks, int threads) {
+    const long long most = (1LL << 31) / threads;
+    return blocks <= most ? dim3((unsigned)blocks) : dim3((unsigned)most, (unsigned)((blocks + most - 1) / most));
+}
+// the block's number in it
+__device__ __forceinline__ unsigned block_number() { return blockIdx.y * gridDim.x + blockIdx.x; }
 // the widest row of the norms: rows held in registers, 1024 threads x 8 accesses
 inline int norm_max_width(bool wide, int dtype) { return 8192 * (wide ? (dtype == KDA_BF16 ? 8 : 4) : 1); }
 hipError_t launch_rmsnorm_fwd(const NormArgs& a);

@@ -92,7 +92,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_fwd_kernel(cons
     constexpr int ROWS = THREADS / TPR;
     __shared__ float slot[TPR > 64 ? 2 * TPR / 64 : 1];
     const int tid = threadIdx.x % TPR;
-    const long long row = (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
+    const long long row = (long long)block_number() * ROWS + threadIdx.x / TPR;
     if (row >= a.rows) return;   // TPR > 64 has one row a block: its threads leave together
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     const T* res = static_cast<const T*>(a.residual);
@@ -312,8 +312,8 @@ hipError_t fwd_n(const NormArgs& a) {
     constexpr int THREADS = TPR < 256 ? 256 : TPR, ROWS = THREADS / TPR;
     const long long blocks = (a.rows + ROWS - 1) / ROWS;
     if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    if (a.scales) hipLaunchKernelGGL((rmsnorm_fwd_kernel<T, VEC, TPR, NV, true>), dim3((unsigned)blocks), dim3(THREADS), 0, a.stream, a);
-    else hipLaunchKernelGGL((rmsnorm_fwd_kernel<T, VEC, TPR, NV, false>), dim3((unsigned)blocks), dim3(THREADS), 0, a.stream, a);
+    if (a.scales) hipLaunchKernelGGL((rmsnorm_fwd_kernel<T, VEC, TPR, NV, true>), grid_of(blocks, THREADS), dim3(THREADS), 0, a.stream, a);
+    else hipLaunchKernelGGL((rmsnorm_fwd_kernel<T, VEC, TPR, NV, false>), grid_of(blocks, THREADS), dim3(THREADS), 0, a.stream, a);
     return hipGetLastError();
 }
 

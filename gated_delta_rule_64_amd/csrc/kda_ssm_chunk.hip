@@ -978,7 +978,7 @@ template <int K> hipError_t launch_k(const SsmArgs& a) {
     const int per = (a.T + C - 1) / C, hblocks = (a.HV + STEP_HEADS - 1) / STEP_HEADS;
     const bool packed = a.cu_seqlens != nullptr;
     const long long chunks = (packed ? (long long)a.T / C + a.N : (long long)a.N * per) * hblocks + 1;
-    if (first > 0x7fffffffLL || second > 0x7fffffffLL || join > 0x7fffffffLL || chunks > 0x7fffffffLL)
+    if (!grid_fits(first, 512) || !grid_fits(second, 256) || !grid_fits(join, K * SLAB / 4 / JOIN_PARTS) || !grid_fits(chunks, 256))
         return hipErrorInvalidConfiguration;
     char* ws = static_cast<char*>(a.workspace);
     p.ends = reinterpret_cast<float*>(ws);

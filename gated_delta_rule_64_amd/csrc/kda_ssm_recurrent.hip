@@ -89,6 +89,7 @@ hipError_t launch_v(const SsmArgs& a) {
     const int nvt = a.V / BV;
     const long long n_items = (long long)a.N * a.HV * nvt;
     if (n_items == 0) return hipSuccess;
+    if (!grid_fits((n_items + 3) / 4, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((ssm_recurrent_kernel<K, BV, TIn>), dim3((unsigned)((n_items + 3) / 4)), dim3(256), 0,
                        a.stream, a, nvt, n_items);
     return hipGetLastError();

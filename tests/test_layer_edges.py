@@ -37,6 +37,12 @@ def test_scan_rows_are_bounded(lib):
     assert size(1, most, 1, 1, 64, 64, 1, 0, 1) >= size(1, most - 64, 1, 1, 64, 64, 1, 0, 1) >= 12 * (most - 64)
 
 
+def test_grids_of_2_to_the_32_threads_are_refused(lib):
+    """HIP counts a launch's threads in 32 bits and would leave the rest out."""
+    for chunk, N in ((False, 2 ** 21), (True, 2 ** 20)):
+        assert ssm(lib, chunk, B=N, N=N, T=1, HV=32, V=64, xs=2048, dts=32) == SHAPE and "grid" in kda.kda_last_error()
+
+
 def test_overlap_is_by_bytes():
     """The binding's check of given outputs, on host tensors."""
     buf = torch.zeros(1000)

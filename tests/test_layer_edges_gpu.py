@@ -239,7 +239,34 @@ def test_conv_backward_of_many_tiles_a_block(i):
     near("dinitial", dh, want[3], 6 * EPS * mag[3] + out * np.abs(want[3]))
 
 
+def test_conv_more_blocks_than_a_grid_has():
+    """Launches of more than 2^32 threads: many sequences of one token, and many channels."""
+    N, D, W = 2 ** 26 + 4, 33, 2
+    x, w = torch.full((N, 1, D), 0.5, dtype=BF, device=DEV), randn(gen(13), D, W, dtype=BF)
+    x[-4:] = 2.0
+    y, _ = kda.kda_conv_fwd(x, w, activation=None)
+    want = (w[:, 1].float()[None] * x[:, 0, :1].float()[[0, -1]]).to(BF)
+    assert torch.equal(y[-4:, 0], want[1].expand(4, -1)) and torch.equal(y[0, 0], want[0])
+    assert torch.equal(y[N // 2], y[0]) and torch.equal(y[2 ** 26 - 1], y[0])
+    del x, y
+    D = 2 ** 27 // 3 + 61
+    x, dy, w = (randn(gen(14 + i), *s, dtype=BF) for i, s in enumerate([(1, 1, D), (1, 1, D), (D, W)]))
+    dx, dw, db, _ = kda.kda_conv_bwd(dy, x, w, w[:, 0].contiguous(), activation=None)
+    assert torch.equal(dw[:, 1], (dy.float() * x.float())[0, 0]) and not dw[:, 0].any() and torch.equal(db, dy.float()[0, 0])
+    assert torch.equal(dx, (dy.float() * w[:, 1].float()).to(BF))
+
+
 # ------------------------------------------------------------------------------ the norm
+def test_norm_more_rows_than_a_grid_has():
+    rows = 2 ** 28 + 16     # sixteen a block of 256 threads
+    x = torch.full((rows, 1), 2.0, dtype=BF, device=DEV)
+    x[-16:] = -3.0
+    y, _, r = kda.kda_rmsnorm_fwd(x, torch.ones(1, dtype=BF, device=DEV), eps=0.0, output_rstd=True)
+    assert (y[:-16] == 1).all() and (y[-16:] == -1).all() and (r[:-16] == 0.5).all() and (r[-16:] == np.float32(1 / 3)).all()
+    q, s, _ = kda.kda_rmsnorm_quant_fwd(x, torch.ones(1, dtype=BF, device=DEV), eps=0.0)
+    assert (q[-16:].float() == -448).all() and (q[::4099].float().abs() == 448).all() and (s[::4099] == np.float32(1 / 448)).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("group", [0, 128])
 def test_norm_codes_are_those_of_the_quotient(group, dtype):
