@@ -178,6 +178,7 @@ int recurrent_impl(const void* q, const void* k, const void* v, const void* g, i
     a.state_vk = state_layout == KDA_STATE_VK ? 1 : 0;
     a.inter_states = inter_states;
     hipError_t err = kda::launch_recurrent(a);
+    if (err == hipErrorInvalidConfiguration) return fail(KDA_ERR_SHAPE, "grid too large");
     if (err != hipSuccess)
         return fail(KDA_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(err));
     return KDA_OK;

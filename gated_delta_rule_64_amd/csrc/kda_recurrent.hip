@@ -181,6 +181,7 @@ hipError_t launch_v(const RecurrentArgs& a) {
     const long long n_items = (long long)a.N * a.HV * nvt;
     if (n_items == 0) return hipSuccess;
     const long long blocks = (n_items + 3) / 4;
+    if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((recurrent_kernel<K, BV, TIn, TB, VK, INTER>), dim3((unsigned)blocks), dim3(256), 0,
                        a.stream, (const TIn*)a.q, (const TIn*)a.k, (const TIn*)a.v, a.g, a.in,
                        (const TB*)a.beta, a.initial_state, a.cu_seqlens, (TIn*)a.o,

@@ -6,6 +6,7 @@ import torch
 
 import gated_delta_rule_64_amd as kda
 from gated_delta_rule_64_amd import _layer, _lib
+from tests.test_abi import _rec, _rec_ex
 from tests.test_layer_abi import OK, SHAPE, ssm
 
 
@@ -41,6 +42,13 @@ def test_grids_of_2_to_the_32_threads_are_refused(lib):
     """HIP counts a launch's threads in 32 bits and would leave the rest out."""
     for chunk, N in ((False, 2 ** 21), (True, 2 ** 20)):
         assert ssm(lib, chunk, B=N, N=N, T=1, HV=32, V=64, xs=2048, dts=32) == SHAPE and "grid" in kda.kda_last_error()
+
+
+def test_decode_grids_of_2_to_the_32_threads_are_refused(lib):
+    _lib.load_library()
+    N = 2 ** 21
+    assert _rec(lib, B=N, N=N, HV=64, V=64) == SHAPE and "grid" in kda.kda_last_error()
+    assert _rec_ex(lib, B=N, N=N, HV=16, V=64, lay=1) == SHAPE and "grid" in kda.kda_last_error()   # 16 columns a wave
 
 
 def test_overlap_is_by_bytes():
