@@ -24,6 +24,7 @@ constexpr int TT_FWD = 32;
 constexpr int TT_BWD = 64;
 constexpr int R = 4;
 constexpr int RB = 2;
+constexpr long long BWD_BLOCKS = 512;
 
 // lanes of a block along the channels (a power of two, at most 64); the block's other lanes
 // take other tiles
@@ -307,12 +308,21 @@ inline long long tiles_of(int B, int T, int N, bool packed, int TT) {
     return packed ? (long long)T / TT + N : (long long)B * tiles_dense_of(T, TT);
 }
 
-// blocks along the rows of the backward, one row of partial sums each: up to 128, then even
-// rounds of them
-inline long long bwd_rows_of_blocks(long long tiles, int groups) {
+// blocks of the backward along the channels
+inline int bwd_dblocks(int D, int vec) {
+    const int cols = lanes_along(D, vec) * vec;
+    return (D + cols - 1) / cols;
+}
+// Blocks along the rows, one row of partial sums each, then even rounds of them: BWD_BLOCKS over
+// all channels (two a unit), and 128 at least. 262144 rows x 256 channels, one block wide: 128
+// blocks 446 us (half the units idle, and a lane's sums four times as long), 512 154, 1024 167;
+// 65536 x 1024 (four wide) 162, 163 and 173; 8192 x 6144 (24 wide) 103 for each.
+inline long long bwd_rows_of_blocks(long long tiles, int D, int vec) {
+    const int groups = 256 / lanes_along(D, vec);
     const long long most = (tiles + groups - 1) / groups;
-    if (most <= 128) return most > 0 ? most : 1;
-    const long long rounds = (most + 127) / 128;
+    const long long cap = BWD_BLOCKS / bwd_dblocks(D, vec) > 128 ? BWD_BLOCKS / bwd_dblocks(D, vec) : 128;
+    if (most <= cap) return most > 0 ? most : 1;
+    const long long rounds = (most + cap - 1) / cap;
     return (most + rounds - 1) / rounds;
 }
 
@@ -337,10 +347,9 @@ template <typename T, int VEC>
 hipError_t bwd_v(const ConvBwdArgs& b) {
     const ConvArgs& a = b.f;
     const int along = lanes_along(a.D, VEC);
-    const int dblocks = (a.D + along * VEC - 1) / (along * VEC);
+    const int dblocks = bwd_dblocks(a.D, VEC);
     const long long tiles = tiles_of(a.B, a.T, a.N, a.cu_seqlens != nullptr, TT_BWD);
-    const int groups = 256 / along;
-    const long long P = bwd_rows_of_blocks(tiles, groups);
+    const long long P = bwd_rows_of_blocks(tiles, a.D, VEC);
     const long long blocks = P * dblocks;
     if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
     const int td = tiles_dense_of(a.T, TT_BWD);
@@ -365,10 +374,10 @@ hipError_t launch_sum_rows(const SumRows& s, hipStream_t stream) {
 }
 
 long long conv_bwd_partials(int B, int T, int D, int N, bool packed) {
-    // the scalar and the 16-byte form differ in their blocks: room for either
+    // the one-channel and the four-channel form differ in their blocks: room for either
     long long most = 0;
     for (int vec : {1, 4}) {
-        const long long P = bwd_rows_of_blocks(tiles_of(B, T, N, packed, TT_BWD), 256 / lanes_along(D, vec));
+        const long long P = bwd_rows_of_blocks(tiles_of(B, T, N, packed, TT_BWD), D, vec);
         most = P > most ? P : most;
     }
     return most;

@@ -21,10 +21,18 @@ def lib():
 @pytest.mark.parametrize("packed", [0, 1])
 @pytest.mark.parametrize("D", [1, 8, 64, 6144])
 def test_conv_workspace_of_the_longest_sequences(lib, D, packed):
-    """Up to 2^31 - 1 rows take about as many partial sums as 2^20: 64 to 128 rows of blocks."""
+    """Up to 2^31 - 1 rows take about as many partial sums as 2^20: 64 to 512 rows of blocks."""
     top = 2 ** 31 - 1
     sizes = [lib.kda_conv_bwd_workspace_bytes(1, T, D, 4, 1, packed, 1) for T in (2 ** 20, top - 130, top - 65, top - 63, top - 31, top)]
-    assert all(64 * 5 * D * 4 <= n <= 128 * 5 * D * 4 for n in sizes), sizes
+    assert all(64 * 5 * D * 4 <= n <= 512 * 5 * D * 4 for n in sizes), sizes
+    assert all(a <= b for a, b in zip(sizes[1:], sizes[2:])), sizes
+
+
+def test_conv_backward_of_narrow_rows_fills_the_units(lib):
+    """Rows of blocks of a long batch: 512 where one block is as wide as a row, 128 for wide rows."""
+    for D, most in ((8, 512), (256, 512), (512, 256), (1024, 128), (6144, 128)):
+        rows = lib.kda_conv_bwd_workspace_bytes(1, 1 << 20, D, 4, 1, 0, 1) / (5 * D * 4)
+        assert 0.9 * most <= rows <= most or (D == 8 and rows == 128), (D, rows)   # 8 channels: 128 tiles a block
 
 
 def test_scan_rows_are_bounded(lib):

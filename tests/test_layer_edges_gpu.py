@@ -215,14 +215,15 @@ def test_conv_longest_sequence():
 
 def conv_sums_case(i):
     rng = np.random.default_rng(20 + i)
-    return [dict(dtype=F32, wdtype=F32, W=4, D=256, B=1, T=34000),
-            dict(dtype=BF, wdtype=BF, W=3, D=200, lens=[int(v) for v in rng.integers(0, 90, 800)], tail=7),
-            dict(dtype=BF, wdtype=F32, W=4, D=252, lens=[1, 0, 2] * 400 + [9000, 63, 64, 65], tail=1)][i]
+    return [dict(dtype=F32, wdtype=F32, W=4, D=1024, B=1, T=34000),
+            dict(dtype=BF, wdtype=BF, W=3, D=449, lens=[int(v) for v in rng.integers(0, 90, 800)], tail=7),
+            dict(dtype=BF, wdtype=F32, W=4, D=1024, lens=[1, 0, 2] * 400 + [9000, 63, 64, 65], tail=1),
+            dict(dtype=BF, wdtype=BF, W=2, D=8, B=1, T=70000)][i]
 
 
-@pytest.mark.parametrize("i", range(3))
+@pytest.mark.parametrize("i", range(4))
 def test_conv_backward_of_many_tiles_a_block(i):
-    """So many rows of so few channels that a block walks several tiles, the last round uneven."""
+    """So many tiles that a block walks several, the last round uneven (and, narrow, one each)."""
     c = conv_case(30 + i, **conv_sums_case(i))
     B, T, D = c["x"].shape
     dy = randn(gen(40 + i), B, T, D, dtype=c["x"].dtype)
