@@ -10,7 +10,8 @@
 // sequence with the window of the last W - 1 rows in registers, so a row is read once, and
 // the W - 1 rows before the tile once more (from L2: the neighbouring tile's lanes read
 // them). A wave is 64 such lanes side by side, one contiguous run of a row per access.
-// 8192 rows of 8192 bf16 channels: 52 us (5.2 TB/s); gradients of 8192 x 6144: 95-98 us.
+// 8192 rows of 8192 bf16 channels: 52 us (5.2 TB/s); gradients of 8192 x 6144: 98 us and 5 for
+// the sum over the blocks' partial sums.
 #include "kda_layer.h"
 
 namespace kda {

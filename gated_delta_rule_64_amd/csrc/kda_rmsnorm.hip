@@ -270,7 +270,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_bwd_kernel(cons
 // takes more threads (8192 x 2048 bf16: one wave of four 19 us, four waves of one 21; 4096 x
 // 8192: four waves of four 36 us, sixteen of one 40; 8192 x 4096: one wave of eight 40 us, four
 // of two 38), the backward, which holds three rows and the weight's sums, with as few as it
-// can (the same sizes: 33 and 25 us, 59 and 44, 89 and 41).
+// can (the same sizes: 33 and 25 us, 59 and 44, 89 and 41). With D above 16384 the backward's
+// rows do not fit its registers (scratch is used): 8192 x 8192 bf16 112 us (4.8 TB/s), 4096 x
+// 16384 127 (4.2), 2048 x 32768 182 (2.9), 1024 x 65536 544 (1.0).
 struct Shape { int tpr, nv; };
 inline Shape shape_of(int n, int vec, bool bwd) {
     if (vec == 4 && n <= 32) return {32, 1};   // 128 fp32 columns are 32 lanes

@@ -17,11 +17,12 @@
 // segments: a first pass forms each segment's own end state (the last one's apart), a small
 // kernel joins them in order (H_(s+1) = L_s + 2^(decay of s) H_s), and the second pass walks
 // every segment from its start state. Both passes read b and x and form the state's update:
-// 60% more matrix work, for as many times more blocks as there are segments.
+// half as much matrix work again, for as many times more blocks as there are segments.
 //
-// 8192 tokens x 32 heads, K = V = 128, bf16: steps 5, first pass 34, join 11, second pass 68
-// us (one pass over the bytes is 40 us at a copy's rate). Matrix, vector and LDS work of the
-// second pass are about equal and overlap little (see the layout notes at the bf16 kernel).
+// 8192 tokens x 32 heads, K = V = 128, bf16: steps 5, first pass 34, join 11, second pass 85
+// us (one pass over the bytes is 33 us at a plain stream's rate). A chunk of the second pass
+// takes a unit about 4,000 cycles of vector, 3,200 of matrix and 2,300 of LDS work a SIMD, which
+// overlap little (see the layout notes at the bf16 kernel).
 #include "kda_layer.h"
 
 namespace kda {
@@ -143,7 +144,8 @@ struct alignas(16) Steps {
 // the exponents are differences of them) and kept as hi + lo. One block: a chunk of a
 // sequence and 8 heads; a wave takes a head, its lane a token. Formed once instead of in
 // every block that walks the chunk, where one wave's transcendentals and 64-bit prefix sums
-// held up the others (first pass of 32768 tokens x 64 heads: 157 us with, 129 without them).
+// held up the others (first pass of 32768 tokens x 64 heads, when they were taken out: 157 us
+// with, 129 without them).
 constexpr int STEP_HEADS = 8;
 
 // inclusive prefix sum over the wave: within the four rows of 16 lanes by lane shifts, then
@@ -532,8 +534,8 @@ template <int LD> __device__ __forceinline__ bf16x4 read_col4(const __bf16* t, i
 __device__ __forceinline__ bf16x8 join(bf16x4 u, bf16x4 v) { return __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7); }
 // a row's 32 elements of step s, in accumulator order: 4 g .. +3 of both halves. Volatile, so
 // that the compiler does not pair the reads: a ds_read2_b64 on this layout takes 16 cycles of
-// LDS, half of them conflicts, where two ds_read_b64 take 4 (scan of 8192 tokens x 32 heads
-// 121 us with pairs, 116 without).
+// LDS, half of them conflicts, where two ds_read_b64 take 4 (scan of 32768 tokens x 64 heads
+// 397 us with pairs, 391 without).
 __device__ __forceinline__ bf16x8 read_row(const __bf16* row, int s) {
     typedef volatile __attribute__((address_space(3))) const bf16x4* lds;
     const bf16x4 u = *(lds)(row + 32 * s), v = *(lds)(row + 32 * s + 16);
@@ -912,9 +914,10 @@ __global__ __launch_bounds__(K * SLAB / 4 / JOIN_PARTS) void ssm_join_kernel(con
 
 // Dense sequences are cut only where their blocks would leave half the chip's 256 units idle
 // (N x units <= 128), into pieces of at least SEG_MIN chunks, for about BLOCKS_WANTED blocks,
-// two a unit: 32768 tokens x 64 heads 362 us (256 blocks 407, 768 396, 1024 384). N x 4096
-// tokens x 32 heads, K = V = 128, cut and whole: N x units = 64 105 and 240 us, 128 184 and
-// 263, 192 267 and 270, 256 313 and 279 (the first pass then costs what the second gains).
+// two a unit: 32768 tokens x 64 heads 419 us (256 blocks 458, 768 450, 1024 436), 8192 x 32 heads
+// 138 (147, 154, 157). N x 4096 tokens x 32 heads, K = V = 128, cut and whole: N x units = 64
+// 132 and 333 us, 128 224 and 340, 192 325 and 346, 256 371 and 352 (the first pass then costs
+// what the second gains).
 constexpr int SEG_MIN = 4;
 constexpr long long BLOCKS_WANTED = 512;
 
@@ -922,15 +925,16 @@ Plan plan_of(int B, int T, int H, int HV, int K, int V, int N, bool packed, int 
     Plan p;
     p.slabs = HV * (V / SLAB);
     // two slabs a block share b, c and their products where a group has an even number of slabs
-    // (32768 tokens x 64 heads: 367 us, one slab a block 428)
+    // (32768 tokens x 64 heads: 419 us, one slab a block 471; 8192 x 32 heads 138 and 147)
     p.ns = dtype == KDA_BF16 && (p.slabs / H) % 2 == 0 ? 2 : 1;
     p.units = p.slabs / p.ns;
     const long long chunks = ((long long)T + C - 1) / C;
     long long seg = chunks > 0 ? chunks : 1;   // chunks of a segment
     if (packed) {
         // lengths are on the device: cut what is longer than twice an even share of the rows
-        // (64 slots of 1..1024 tokens x 16 heads: 180 us, with once a share 255: the first pass
-        // then works on a few sequences only, in order)
+        // (64 slots of 1..1024 tokens x 16 heads: 182 us, with once a share 242: the first pass
+        // then works on a few sequences only, in order; one prompt of 8192 x 32 heads takes 138 us
+        // either way, and as a dense one)
         const long long share = 2 * chunks * p.units / BLOCKS_WANTED;
         const long long piece = share > SEG_MIN ? share : SEG_MIN;
         if (piece < seg) seg = piece;
